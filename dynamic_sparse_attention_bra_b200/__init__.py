@@ -14,6 +14,15 @@ Entry points (same names as the C ABI):
     bra_forward(shape, q, k, v, o, idx, workspace, stream=None)
     bra_device_status(shape, workspace, stream=None)
 
+the operators around the attention in a conditioned block, whose shapes
+come from their tensors (``cross_shape_for``, ``rotary_shape_for``):
+
+    bra_cross_attend(shape, q, k, v, kv_len, kv_mask, o, lse, workspace, stream=None)
+    bra_cross_attend_backward(shape, q, k, v, kv_len, kv_mask, o, lse, grad_o,
+                              dq, dk, dv, workspace, stream=None)
+    bra_rotary(shape, q, k, pos, inv_freq, q_out, k_out, stream=None)
+    bra_dropout_add(x, residual, p, rng, y, unit=1, stream=None)
+
 and a convenience wrapper ``forward(q, k, v, heads, S, topk)`` that
 allocates the outputs and workspace with torch and returns ``(o, idx)``.
 """
@@ -27,6 +36,9 @@ __all__ = [
     "bra_forward", "bra_device_status", "bra_status_string", "forward", "library_path",
     "bra_route_noalloc", "bra_lce", "bra_selftest_bounded_wait", "bra_attend_backward",
     "bra_qkv_project", "bra_forward_qkv", "bra_forward_lce", "EXPORTED_SYMBOLS",
+    "BraCrossShape", "cross_shape_for", "bra_cross_workspace_bytes", "bra_cross_attend",
+    "bra_cross_attend_backward", "bra_cross_device_status", "cross_attention",
+    "BraRotaryShape", "rotary_shape_for", "bra_rotary", "bra_dropout_add",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +54,8 @@ BRA_DTYPE_F32, BRA_DTYPE_BF16 = 0, 1
 EXPORTED_SYMBOLS = ("bra_workspace_bytes", "bra_route", "bra_attend", "bra_forward",
                     "bra_device_status", "bra_status_string", "bra_version", "bra_route_noalloc",
                     "bra_lce", "bra_selftest_bounded_wait", "bra_attend_backward", "bra_qkv_project",
-                    "bra_forward_qkv", "bra_forward_lce")
+                    "bra_forward_qkv", "bra_forward_lce", "bra_cross_workspace_bytes", "bra_cross_attend",
+                    "bra_cross_attend_backward", "bra_cross_device_status", "bra_rotary", "bra_dropout_add")
 NOALLOC_MAX_MEANS = 1 << 20  # BRA_NOALLOC_MAX_MEANS
 
 
@@ -51,6 +64,22 @@ class BraShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("W", ctypes.c_int), ("C", ctypes.c_int),
                 ("heads", ctypes.c_int), ("S", ctypes.c_int), ("topk", ctypes.c_int),
                 ("dtype", ctypes.c_int)]
+
+
+class BraCrossShape(ctypes.Structure):
+    """Mirror of ``bra_cross_shape``."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "Lq", "Lk", "heads", "kv_heads", "d", "dtype")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_row", "q_batch", "k_row", "k_batch", "v_row", "v_batch")])
+
+
+class BraRotaryShape(ctypes.Structure):
+    """Mirror of ``bra_rotary_shape``."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "T", "H", "W", "heads", "kv_heads", "d")]
+                + [("pairs", ctypes.c_int * 3)]
+                + [(n, ctypes.c_int) for n in ("interleaved", "inverse", "dtype")]
+                + [(n, ctypes.c_int64) for n in ("pos_batch", "q_row", "q_batch", "k_row", "k_batch", "qo_row",
+                                                 "qo_batch", "ko_row", "ko_batch")])
 
 
 class BraError(RuntimeError):
@@ -80,6 +109,17 @@ def _load() -> ctypes.CDLL:
     lib.bra_route_noalloc.argtypes = [sp, vp, vp, vp, vp]
     lib.bra_route_noalloc.restype = ctypes.c_int
     for f in (lib.bra_route, lib.bra_attend, lib.bra_forward, lib.bra_device_status):
+        f.restype = ctypes.c_int
+    cp, rp = ctypes.POINTER(BraCrossShape), ctypes.POINTER(BraRotaryShape)
+    lib.bra_cross_workspace_bytes.argtypes = [cp]
+    lib.bra_cross_workspace_bytes.restype = ctypes.c_size_t
+    lib.bra_cross_attend.argtypes = [cp] + [vp] * 9
+    lib.bra_cross_attend_backward.argtypes = [cp] + [vp] * 13
+    lib.bra_cross_device_status.argtypes = [cp, vp, vp]
+    lib.bra_rotary.argtypes = [rp] + [vp] * 7
+    lib.bra_dropout_add.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_double] + [vp] * 5
+    for f in (lib.bra_cross_attend, lib.bra_cross_attend_backward, lib.bra_cross_device_status, lib.bra_rotary,
+              lib.bra_dropout_add):
         f.restype = ctypes.c_int
     lib.bra_status_string.argtypes = [ctypes.c_int]
     lib.bra_status_string.restype = ctypes.c_char_p
@@ -216,3 +256,226 @@ def forward(q, k, v, heads: int, S: int, topk: int, stream=None):
     idx = torch.empty((B, heads, S * S, topk), dtype=torch.int32, device=q.device)
     bra_forward(shape, q, k, v, o, idx, ws, stream)
     return o, idx
+
+
+# ---- operators around the attention: shapes and strides come from tensors ----
+
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BRA_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return BRA_DTYPE_F32
+    raise ValueError(f"expected a bfloat16 or float32 tensor, got {t.dtype}")
+
+
+def _token_strides(t, name: str, width: int):
+    """(B, L, row step, entry step) in elements of tokens [B, L, width], or of
+    a contiguous map [B, H, W, width] (or [B, T, H, W, width])."""
+    if t.ndim != 3:
+        if t.ndim < 3 or t.shape[-1] != width or not t.is_contiguous():
+            raise ValueError(f"{name}: expected [B, L, {width}] or a contiguous map, got {tuple(t.shape)}")
+        B, L = t.shape[0], 1
+        for n in t.shape[1:-1]:
+            L *= n
+        return B, L, width, L * width
+    B, L, w = t.shape
+    sb, sl, se = t.stride()
+    if w != width or (se != 1 and w > 1):
+        raise ValueError(f"{name}: expected [B, L, {width}] with consecutive elements, got {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    row = sl if L > 1 else width  # a step that is never taken is the dense one
+    return B, L, row, sb if B > 1 else L * row
+
+
+def _same_tokens(t, name, width, B, L, row, batch, dtype, device):
+    """``t`` is what the shape says: its size, steps, type and device."""
+    if _dtype_code(t) != dtype or t.device != device:
+        raise ValueError(f"{name}: expected the shape's type on {device}, got {t.dtype} on {t.device}")
+    if _token_strides(t, name, width) != (B, L, row, batch):
+        raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} is not what the shape says")
+
+
+def _dense(t, name, dtype, numel, device):
+    if t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on {device}")
+
+
+def _call(where: str, fn, device, stream, *args):
+    """``fn(*args, stream)`` with ``device`` current; None is its current stream."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{where}: expected CUDA tensors, got {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != BRA_OK:
+        raise BraError(status, where)
+
+
+def cross_shape_for(q, k, v, heads: int, kv_heads: int | None = None, scale: float | None = None) -> BraCrossShape:
+    """``bra_cross_shape`` of q [B, Lq, heads * d] (or a contiguous map) and k, v
+    [B, Lk, kv_heads * d]; the three may be slices or (in B) expanded views.
+    ``scale`` defaults to 1 / sqrt(d)."""
+    kv_heads = heads if kv_heads is None else kv_heads
+    dtype = _dtype_code(q)
+    wq = q.shape[-1]
+    if heads < 1 or kv_heads < 1 or wq % heads:
+        raise ValueError(f"{heads} heads do not divide {wq} channels")
+    d = wq // heads
+    B, Lq, q_row, q_batch = _token_strides(q, "q", wq)
+    Bk, Lk, k_row, k_batch = _token_strides(k, "k", kv_heads * d)
+    Bv, Lv, v_row, v_batch = _token_strides(v, "v", kv_heads * d)
+    if (Bk, Bv) != (B, B) or Lk != Lv or _dtype_code(k) != dtype or _dtype_code(v) != dtype:
+        raise ValueError("q, k and v disagree in batch, length or type")
+    return BraCrossShape(B, Lq, Lk, heads, kv_heads, d, dtype, d ** -0.5 if scale is None else scale, q_row, q_batch,
+                         k_row, k_batch, v_row, v_batch)
+
+
+def _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace):
+    import torch
+    dev = q.device
+    _same_tokens(q, "q", s.heads * s.d, s.B, s.Lq, s.q_row, s.q_batch, s.dtype, dev)
+    _same_tokens(k, "k", s.kv_heads * s.d, s.B, s.Lk, s.k_row, s.k_batch, s.dtype, dev)
+    _same_tokens(v, "v", s.kv_heads * s.d, s.B, s.Lk, s.v_row, s.v_batch, s.dtype, dev)
+    if kv_len is not None:
+        _dense(kv_len, "kv_len", torch.int32, s.B, dev)
+    if kv_mask is not None:
+        if kv_mask.dtype == torch.bool:
+            kv_mask = kv_mask.view(torch.uint8)
+        _dense(kv_mask, "kv_mask", torch.uint8, s.B * s.Lk, dev)
+    _dense(workspace, "workspace", torch.uint8, bra_cross_workspace_bytes(s), dev)
+    return dev, kv_mask
+
+
+def bra_cross_workspace_bytes(shape: BraCrossShape) -> int:
+    return int(_lib.bra_cross_workspace_bytes(ctypes.byref(shape)))
+
+
+def bra_cross_attend(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o, lse, workspace, stream=None) -> None:
+    """o [B, Lq, heads * d] (and lse fp32 [B, heads, Lq], or None) of q over the
+    states k, v; kv_len int32 [B] and kv_mask uint8 or bool [B, Lk], or None,
+    say which states are valid.  ``workspace``: bra_cross_workspace_bytes(shape)
+    bytes of uint8, zeroed once."""
+    import torch
+    s = shape
+    dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
+    _dense(o, "o", q.dtype, s.B * s.Lq * s.heads * s.d, dev)
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, s.B * s.Lq * s.heads, dev)
+    _call("bra_cross_attend", _lib.bra_cross_attend, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v),
+          _ptr(kv_len), _ptr(kv_mask), _ptr(o), _ptr(lse), _ptr(workspace))
+
+
+def bra_cross_attend_backward(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o, lse, grad_o, dq, dk, dv, workspace,
+                              stream=None) -> None:
+    """dq, dk, dv (dense, of q's type, overwritten) for the gradient grad_o of
+    bra_cross_attend's o; o and lse as it wrote them."""
+    import torch
+    s = shape
+    dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
+    nq, nk = s.B * s.Lq * s.heads * s.d, s.B * s.Lk * s.kv_heads * s.d
+    for t, name, n in ((o, "o", nq), (grad_o, "grad_o", nq), (dq, "dq", nq), (dk, "dk", nk), (dv, "dv", nk)):
+        _dense(t, name, q.dtype, n, dev)
+    _dense(lse, "lse", torch.float32, s.B * s.Lq * s.heads, dev)
+    _call("bra_cross_attend_backward", _lib.bra_cross_attend_backward, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k),
+          _ptr(v), _ptr(kv_len), _ptr(kv_mask), _ptr(o), _ptr(lse), _ptr(grad_o), _ptr(dq), _ptr(dk), _ptr(dv),
+          _ptr(workspace))
+
+
+def bra_cross_device_status(shape: BraCrossShape, workspace, stream=None) -> int:
+    """Synchronises the stream; returns (and clears) the device status code."""
+    return int(_lib.bra_cross_device_status(ctypes.byref(shape), _ptr(workspace), _stream(stream)))
+
+
+def cross_attention(q, k, v, heads: int, kv_heads: int | None = None, kv_len=None, kv_mask=None,
+                    scale: float | None = None, stream=None):
+    """(o, lse) of q [B, Lq, heads * d] over the states k, v [B, Lk, kv_heads * d].
+
+    Allocates o, lse and a zeroed workspace with torch on q's device, then runs
+    ``bra_cross_attend``."""
+    import torch
+    shape = cross_shape_for(q, k, v, heads, kv_heads, scale)
+    nbytes = bra_cross_workspace_bytes(shape)
+    if nbytes == 0:
+        raise BraError(BRA_ERR_INVALID_ARG if shape.d in (32, 64, 128) else BRA_ERR_UNSUPPORTED, "cross_attention")
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((shape.B, heads, shape.Lq), dtype=torch.float32, device=q.device)
+    bra_cross_attend(shape, q, k, v, kv_len, kv_mask, o, lse, ws, stream)
+    return o, lse
+
+
+def rotary_shape_for(q, k, heads: int, kv_heads: int, pairs, grid=None, pos=None, interleaved: bool = False,
+                     inverse: bool = False, q_out=None, k_out=None) -> BraRotaryShape:
+    """``bra_rotary_shape`` of q [B, L, heads * d] and k [B, L, kv_heads * d] (or
+    None).  ``pairs``: rotation pairs of (time, height, width).  ``grid``: (T,
+    H, W) of the L tokens, or None for a sequence (time runs over L).  ``pos``:
+    the positions int32 [B, L, 3] (or [1, L, 3], shared) that the calls will be
+    given, if any.  ``q_out``, ``k_out``: outputs that are not dense."""
+    wq = q.shape[-1]
+    if heads < 1 or wq % heads:
+        raise ValueError(f"{heads} heads do not divide {wq} channels")
+    d = wq // heads
+    B, L, q_row, q_batch = _token_strides(q, "q", wq)
+    T, H, W = (L, 1, 1) if grid is None else grid
+    if T * H * W != L:
+        raise ValueError(f"a grid of {T} x {H} x {W} has no {L} tokens")
+    k_row = k_batch = ko_row = ko_batch = 0
+    qo_row, qo_batch = wq, L * wq
+    if q_out is not None:
+        qo_row, qo_batch = _token_strides(q_out, "q_out", wq)[2:]
+    if k is not None:
+        wk = kv_heads * d
+        Bk, Lk, k_row, k_batch = _token_strides(k, "k", wk)
+        if (Bk, Lk) != (B, L) or _dtype_code(k) != _dtype_code(q):
+            raise ValueError("q and k disagree in batch, length or type")
+        ko_row, ko_batch = wk, L * wk
+        if k_out is not None:
+            ko_row, ko_batch = _token_strides(k_out, "k_out", wk)[2:]
+    pos_batch = L * 3 if pos is not None and pos.shape[0] > 1 else 0
+    return BraRotaryShape(B, T, H, W, heads, kv_heads if k is not None else 0, d, tuple(pairs), int(interleaved),
+                          int(inverse), _dtype_code(q), pos_batch, q_row, q_batch, k_row, k_batch, qo_row, qo_batch,
+                          ko_row, ko_batch)
+
+
+def bra_rotary(shape: BraRotaryShape, q, k, pos, inv_freq, q_out, k_out, stream=None) -> None:
+    """q_out, k_out = q, k turned by their positions: pos int32 [B or 1, L, 3]
+    (time, height, width), or None for the shape's grid; inv_freq fp32, one for
+    each pair.  k and k_out may both be None."""
+    import torch
+    s, dev = shape, q.device
+    L, wq, wk = s.T * s.H * s.W, s.heads * s.d, s.kv_heads * s.d
+    _same_tokens(q, "q", wq, s.B, L, s.q_row, s.q_batch, s.dtype, dev)
+    _same_tokens(q_out, "q_out", wq, s.B, L, s.qo_row, s.qo_batch, s.dtype, dev)
+    if (k is None) != (k_out is None) or (k is None) != (s.kv_heads == 0):
+        raise ValueError("k, k_out and the shape's kv_heads go together")
+    if k is not None:
+        _same_tokens(k, "k", wk, s.B, L, s.k_row, s.k_batch, s.dtype, dev)
+        _same_tokens(k_out, "k_out", wk, s.B, L, s.ko_row, s.ko_batch, s.dtype, dev)
+    if pos is not None:
+        _dense(pos, "pos", torch.int32, (s.B - 1) * s.pos_batch + L * 3 if s.B else 0, dev)
+    _dense(inv_freq, "inv_freq", torch.float32, sum(s.pairs), dev)
+    _call("bra_rotary", _lib.bra_rotary, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(pos), _ptr(inv_freq),
+          _ptr(q_out), _ptr(k_out))
+
+
+def bra_dropout_add(x, residual, p: float, rng, y, unit: int = 1, stream=None) -> None:
+    """y = residual + (keep ? x / (1 - p) : 0), ``unit`` consecutive elements
+    sharing a draw (see include/bra.h); residual may be None, rng is an int64
+    (or uint64) tensor {seed, offset} on x's device.  The gradient of x is the
+    same call on the gradient of y, without a residual."""
+    import torch
+    n, dev = x.numel(), x.device
+    dtype = _dtype_code(x)
+    for t, name in ((x, "x"), (residual, "residual"), (y, "y")):
+        if t is not None:
+            _dense(t, name, x.dtype, n, dev)
+    _dense(rng, "rng", torch.uint64 if rng.dtype == torch.uint64 else torch.int64, 2, dev)
+    _call("bra_dropout_add", _lib.bra_dropout_add, dev, stream, dtype, n, unit, p, _ptr(rng), _ptr(x), _ptr(residual),
+          _ptr(y))

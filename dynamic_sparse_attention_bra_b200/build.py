@@ -23,6 +23,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-warn-spills",
+    "--threads", "0",  # the sources in parallel
 ]
 
 

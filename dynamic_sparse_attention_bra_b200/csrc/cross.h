@@ -1,0 +1,80 @@
+// Cross attention to an encoder's states: geometry and launchers (internal).
+#pragma once
+
+#include <cstddef>
+
+#include "../../include/bra.h"
+#include "common.cuh"
+
+namespace bra {
+
+// One call's geometry.  The query heads of a state head form its group (rep
+// of them); the group's rows are numbered r = t * rep + (head in the group),
+// so that the rows of one token are consecutive in memory.
+struct CrossGeom {
+    int B, Lq, Lk, heads, kv_heads, rep, d;
+    int rows;  // rep * Lq
+    float scale;
+    long long q_row, q_batch, k_row, k_batch, v_row, v_batch;  // strides in elements
+    const int32_t* kv_len;   // [B] or null
+    const uint8_t* kv_mask;  // [B, Lk] or null
+};
+
+// Valid states of entry b: kv_len clamped to [0, Lk] (the mask not counted).
+__device__ __forceinline__ int cross_len(const CrossGeom& g, int b) {
+    if (!g.kv_len) return g.Lk;
+    const int n = __ldcg(g.kv_len + b);
+    return n < 0 ? 0 : (n > g.Lk ? g.Lk : n);
+}
+// Element offsets of row r (see above) of entry b, state head j.
+__device__ __forceinline__ size_t cross_q_offset(const CrossGeom& g, int b, int j, int r) {
+    const int t = r / g.rep, hh = r - t * g.rep;
+    return (size_t)b * g.q_batch + (size_t)t * g.q_row + (size_t)(j * g.rep + hh) * g.d;
+}
+// ... of O, dO and dQ, which are dense [B, Lq, heads, d].
+__device__ __forceinline__ size_t cross_o_offset(const CrossGeom& g, int b, int j, int r) {
+    const int t = r / g.rep, hh = r - t * g.rep;
+    return (((size_t)b * g.Lq + t) * g.heads + (size_t)(j * g.rep + hh)) * g.d;
+}
+// ... of the log sums and D, [B, heads, Lq].
+__device__ __forceinline__ size_t cross_lse_offset(const CrossGeom& g, int b, int j, int r) {
+    const int t = r / g.rep, hh = r - t * g.rep;
+    return ((size_t)b * g.heads + (size_t)(j * g.rep + hh)) * g.Lq + t;
+}
+
+// Partial results of a key split: rows x d unnormalised sums, then (maximum in
+// powers of two, sum) pairs, for every (split, entry, state head, row).
+struct CrossParts {
+    float* o;
+    float2* ml;
+};
+
+// How a forward call is cut: by its sizes alone, so that the workspace's size
+// follows from the shape.
+struct CrossPlan {
+    int splits;  // parts of the states, joined by a second kernel (1: none)
+};
+CrossPlan cross_forward_plan(const CrossGeom& g, bool bf16);
+size_t cross_forward_part_rows(const CrossGeom& g, const CrossPlan& p);  // 0 without a split
+
+bra_status cross_forward_bf16(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,
+                              void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream);
+bra_status cross_forward_f32(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,
+                             void* o, float* lse, CrossParts parts, cudaStream_t stream);
+// Joins the parts of a split into o and lse.
+bra_status cross_join(const CrossGeom& g, int splits, bool bf16, CrossParts parts, void* o, float* lse,
+                      cudaStream_t stream);
+
+// Backward: splits of the rows in the dK, dV kernel, whose fp32 parts
+// ([split][2][B, Lk, kv_heads, d]) a second kernel joins.
+int cross_backward_splits(const CrossGeom& g, bool bf16);
+bra_status cross_backward_bf16(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
+                               const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
+                               float* delta, float* parts, int* status, cudaStream_t stream);
+bra_status cross_backward_f32(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
+                              const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
+                              float* delta, float* parts, cudaStream_t stream);
+bra_status cross_backward_join(const CrossGeom& g, int splits, bool bf16, const float* parts, void* dk, void* dv,
+                               cudaStream_t stream);
+
+}  // namespace bra

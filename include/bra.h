@@ -284,6 +284,144 @@ bra_status bra_forward_qkv(const bra_shape* shape, const void* x, const void* w_
 bra_status bra_selftest_bounded_wait(const bra_shape* shape, void* workspace, unsigned int tries, int arrive,
                                      void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the attention in a conditioned block: a map's tokens (or a
+ * decoder's) that also read an encoder's states, rotary positions, and dropout
+ * with the residual's sum.  They take shapes of their own; ownership,
+ * asynchrony, alignment (16 bytes) and errors are as above: an invalid call
+ * returns an error and launches nothing, and nothing is allocated.  All
+ * buffers and the stream belong to the calling thread's current device.
+ */
+
+/*
+ * Cross attention: Lq query tokens and Lk encoder states of each of B
+ * entries.  ``heads`` query heads of size d read ``kv_heads`` state heads
+ * (kv_heads divides heads; head h reads state head h / (heads / kv_heads)).
+ * A token's heads are consecutive: Q, O [B, Lq, heads, d]; K, V [B, Lk,
+ * kv_heads, d].  Q, K and V may be slices of larger tensors: *_row and *_batch
+ * are the elements from a token, and from an entry, to the next (multiples of
+ * 16 bytes; a row step is at least the row unless there is one token; a
+ * batch step of 0 gives every entry the same tokens).  O, gradients and
+ * lse are dense.  Limits: d in {32, 64, 128}, B <= 65535, heads <= 1024,
+ * Lq * heads <= 2^28, Lk <= 2^28.  B, Lq and Lk may be 0.
+ */
+typedef struct {
+    int B, Lq, Lk;
+    int heads, kv_heads, d;
+    int dtype;   /* a bra_dtype */
+    float scale; /* of the logits; finite and positive, 1/sqrt(d) as a rule */
+    int64_t q_row, q_batch, k_row, k_batch, v_row, v_batch;
+} bra_cross_shape;
+
+/*
+ * Bytes of device workspace for the calls below with ``shape``: a 256-byte
+ * status block (zero it once), D of the backward, parts of a split.  0 when
+ * ``shape`` is invalid.  Calls that share a workspace must be ordered on the
+ * GPU.  The size depends on the current device's number of SMs.
+ */
+size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
+
+/*
+ * For every query token t and head h of entry b, over the valid states j:
+ *   s_j = scale <q_t, k_j>,  O_t = sum_j softmax_j(s) v_j,
+ *   lse_t = log sum_j exp(s_j).
+ * State j is valid if j < kv_len[b] and kv_mask[b, j] != 0.  Invalid states
+ * are not read: they may hold anything.  A token without valid states gets
+ * O = 0 and lse = -infinity.  Any number of tokens runs: few (a decoder's next
+ * token) split the states over the GPU.
+ *   kv_len     device int32 [B], or NULL (all Lk); values are clamped to [0, Lk]
+ *   kv_mask    device uint8 [B, Lk] (any nonzero byte: valid), or NULL
+ *   o          device [B, Lq, heads, d] of ``shape->dtype``, written
+ *   lse        device fp32 [B, heads, Lq], written (the backward needs it), or NULL
+ *   workspace  device, bra_cross_workspace_bytes(shape) bytes
+ * bf16: products on tensor cores with fp32 sums, the softmax in fp32, P
+ * rounded once to bf16 as an operand, O rounded once.  fp32: CUDA cores, fp32
+ * throughout.  The same inputs give the same bits.
+ * Errors: BRA_ERR_INVALID_ARG, BRA_ERR_UNSUPPORTED (another d, or past the
+ * limits), BRA_ERR_CUDA.
+ */
+bra_status bra_cross_attend(const bra_cross_shape* shape, const void* q, const void* k, const void* v,
+                            const int32_t* kv_len, const uint8_t* kv_mask, void* o, float* lse, void* workspace,
+                            void* stream);
+
+/*
+ * Gradients of bra_cross_attend: with dP = dO V^T, D_t = <dO_t, O_t> and
+ * dS = P (dP - D),
+ *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+ * dK and dV summed over the query heads that read a state head.  Invalid
+ * states and tokens without valid states get zeros.  With a batch step of 0
+ * each entry still gets its own dK and dV.
+ *   o, lse      as bra_cross_attend wrote them
+ *   grad_o      device [B, Lq, heads, d] of ``shape->dtype``, dense
+ *   dq, dk, dv  device, dense, of ``shape->dtype``, every element written
+ *               (sums in fp32, in a fixed order, rounded once)
+ */
+bra_status bra_cross_attend_backward(const bra_cross_shape* shape, const void* q, const void* k, const void* v,
+                                     const int32_t* kv_len, const uint8_t* kv_mask, const void* o, const float* lse,
+                                     const void* grad_o, void* dq, void* dk, void* dv, void* workspace,
+                                     void* stream);
+
+/* bra_device_status for a cross-attention workspace. */
+bra_status bra_cross_device_status(const bra_cross_shape* shape, void* workspace, void* stream);
+
+/*
+ * Rotary positions with several axes on Q [B, L, heads, d] and K [B, L,
+ * kv_heads, d], L = T * H * W tokens of a video, an image (T = 1) or a
+ * sequence (H = W = 1).  The first pairs[0] rotation pairs of a head turn with
+ * the token's time, the next pairs[1] with its height, the next pairs[2] with
+ * its width; with P = pairs[0] + pairs[1] + pairs[2] (1 <= P <= d / 2), pair
+ * i is the channels (i, i + P), or (2 i, 2 i + 1) if ``interleaved``;
+ * channels from 2 P on are copied.  Strides as for bra_cross_shape, of the
+ * inputs and of the outputs.  Limits: d a multiple of 8, at most 512; B <= 65535,
+ * heads <= 1024, L <= 2^28.  B and L may be 0.
+ */
+typedef struct {
+    int B, T, H, W;
+    int heads, kv_heads, d;
+    int pairs[3];
+    int interleaved;
+    int inverse; /* turn the other way: the gradient of the rotation */
+    int dtype;   /* a bra_dtype */
+    int64_t pos_batch; /* elements between two entries' positions; 0: shared */
+    int64_t q_row, q_batch, k_row, k_batch, qo_row, qo_batch, ko_row, ko_batch;
+} bra_rotary_shape;
+
+/*
+ * Pair i turns by pos[axis(i)] * inv_freq[i] radians:
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
+ * the angle formed and reduced in fp64, the rotation in fp32, rounded once.
+ *   pos       device int32 [B or 1, L, 3] (time, height, width of each token),
+ *             or NULL: token l = (t * H + y) * W + x is at (t, y, x)
+ *   inv_freq  device fp32 [P]: one frequency for each pair (any base or layout)
+ *   q_out, k_out  written; either may be its input (with equal strides), other
+ *             overlaps are not allowed
+ * K is optional: k = k_out = NULL.
+ */
+bra_status bra_rotary(const bra_rotary_shape* shape, const void* q, const void* k, const int32_t* pos,
+                      const float* inv_freq, void* q_out, void* k_out, void* stream);
+
+/*
+ * Dropout with the residual's sum; the mask is drawn anew wherever it is
+ * needed and never stored:
+ *   y[i] = residual[i] + (keep(i / unit) ? x[i] / (1 - p) : 0).
+ * Draw u is word u % 4 of Philox4x32-10 with key rng[0] and counter
+ * rng[1] + u / 4 (64-bit, wrapping; the counter's upper half is 0); it keeps
+ * its unit where the word is at least p * 2^32.  unit = 1 drops elements, a
+ * token's or a sample's elements drop tokens or whole samples (stochastic
+ * depth).  A dropped x is not read into the sum, whatever it holds.  The
+ * gradient of x is the same call on dy with residual = NULL; that of the
+ * residual is dy.  A call uses ceil(ceil(n / unit) / 4) counters.
+ *   dtype     a bra_dtype, of x, residual and y (n dense elements each)
+ *   unit      1 or a multiple of 8 (else BRA_ERR_UNSUPPORTED)
+ *   p         in [0, 1]
+ *   rng       device uint64 [2]: seed and offset, read when the kernel runs
+ *   residual  or NULL (0)
+ *   y         written; it may be x or residual
+ */
+bra_status bra_dropout_add(int dtype, int64_t n, int64_t unit, double p, const uint64_t* rng, const void* x,
+                           const void* residual, void* y, void* stream);
+
 /* Static English text for a status code. */
 const char* bra_status_string(bra_status status);
 

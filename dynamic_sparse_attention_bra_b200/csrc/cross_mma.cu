@@ -356,7 +356,8 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 }
 
 int rows_per_cta(const CrossGeom& g, bool bf16) {
-    if (!bf16) return 64;
+    if (!bf16) return g.rows <= 16 ? 16 : 64;
+    if (cross_tc_covers(g)) return cross_tc_rows();
     return g.rows <= 16 ? 16 : (g.d == 32 ? 128 : 64);
 }
 
@@ -384,8 +385,8 @@ size_t cross_forward_part_rows(const CrossGeom& g, const CrossPlan& p) {
 
 bra_status cross_forward_bf16(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,
                               void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream) {
-    (void)status;
-    const bra_status rc = g.d == 32   ? launch_d<32>(g, p.splits, q, k, v, o, lse, parts, stream)
+    const bra_status rc = cross_tc_covers(g) ? cross_forward_tc(g, p.splits, q, k, v, o, lse, parts, status, stream)
+                          : g.d == 32   ? launch_d<32>(g, p.splits, q, k, v, o, lse, parts, stream)
                           : g.d == 64 ? launch_d<64>(g, p.splits, q, k, v, o, lse, parts, stream)
                                       : launch_d<128>(g, p.splits, q, k, v, o, lse, parts, stream);
     if (rc != BRA_OK || p.splits == 1) return rc;

@@ -23,7 +23,7 @@ struct CrossGeom {
 // Valid states of entry b: kv_len clamped to [0, Lk] (the mask not counted).
 __device__ __forceinline__ int cross_len(const CrossGeom& g, int b) {
     if (!g.kv_len) return g.Lk;
-    const int n = __ldcg(g.kv_len + b);
+    const int n = g.kv_len[b];
     return n < 0 ? 0 : (n > g.Lk ? g.Lk : n);
 }
 // Element offsets of row r (see above) of entry b, state head j.

@@ -371,9 +371,11 @@ CrossPlan cross_forward_plan(const CrossGeom& g, bool bf16) {
     if (sms <= 0 || g.Lk < 512) return p;
     const int rpc = rows_per_cta(g, bf16);
     const long long ctas = (long long)((g.rows + rpc - 1) / rpc) * g.kv_heads * g.B;
-    if (ctas <= 0 || ctas >= 2LL * sms) return p;
-    long long s = (4LL * sms) / ctas;
-    const long long most = g.Lk / 256;
+    // the many-row form has one CTA of 256 rows on an SM; the others several small ones
+    const bool tc = bf16 && cross_tc_covers(g);
+    if (ctas <= 0 || ctas >= (tc ? 1LL : 2LL) * sms) return p;
+    long long s = (tc ? 1LL : 4LL) * sms / ctas;
+    const long long most = g.Lk / (tc ? 512 : 256);
     if (s > most) s = most;
     p.splits = s < 1 ? 1 : (int)s;
     return p;

@@ -3,21 +3,27 @@
 // is that of cross_mma.cu.
 //
 // A unit of work is 256 rows of one (entry, state head), two tiles of 128, and
-// a range of the states, streamed in blocks of 64 that both tiles share.  Per
-// tile and block: S = Q K^T (M 128, N up to 64) lands in TMEM; a softmax
-// thread per row reads its scores twice (maximum, then exponentials), writes P
-// as bf16 into TMEM, and O += P V (P the TMEM operand, N = d) accumulates in
-// TMEM.  O is rescaled only where a row's maximum has grown by more than 2^8
+// a range of the states, streamed in blocks of 128 (64 at d = 128) that both tiles
+// share.  Per tile and block: S = Q K^T (M 128, N = the block) lands in TMEM; a softmax
+// thread per row takes its scores into registers, writes P as bf16 into TMEM,
+// and O += P V (P the TMEM operand, N = d) accumulates in TMEM.  O is rescaled only where a row's maximum has grown by more than 2^8
 // since the last rescale (until then P may exceed 1: its relative rounding
 // is the same, and l, in fp32, uses the same offset), so that the common
 // block costs no pass over O.
 //
-// Roles of the 12 warps: 0, 1 issue the products of tile 0, 1; 2, 3 load (16-byte
-// cp.async, masked or missing rows filled with zeros: blocks of the states in turn,
-// and the tile's Q, double-buffered); 4-7, 8-11 are the tiles' softmax.  Two
-// such CTAs run on an SM for d <= 64 (256 TMEM columns each), one for d = 128.
-// For d = 64 P takes S's columns, and the next S waits for P V; otherwise P has
-// columns of its own, and the next S is issued before P V.
+// Roles of the 11 warps, one CTA on an SM: 0, 1 issue the products of tile 0, 1;
+// 2 loads the blocks of K and V, and both tiles' Q (double-buffered), by TMA, a
+// block with a masked state, or past the entry's last, by 16-byte cp.async that
+// fill the missing rows with zeros, so that what is stored there never reaches a
+// product; 3-6, 7-10 are the tiles' softmax.  For d <= 64 the next S is issued as
+// soon as the scores are in registers, under the exponentials.  For d = 128 the
+// columns do not suffice for a P of its own: P takes its S's, and S has two
+// buffers, so that the next S is there before this softmax ends.
+//
+// Blocks of 64 for d <= 64, with two CTAs of 96 registers a thread on an SM, and
+// with one CTA and two buffers of S and P, were slower (127 and 168 us where this
+// form takes HIGHRES, 16384 rows over 4096 states): a block's waits and the
+// latency of its score load cost about 900 clocks whatever its width.
 //
 // Bound by the exponentials (16 a clock and SM) for d = 32, by them and the
 // products for d = 128.  Every mbarrier wait is bounded; on expiry the kernel
@@ -31,31 +37,35 @@ namespace {
 
 using namespace cross;
 
-constexpr int kCtrl = 4;
+constexpr int kCtrl = 3;
 constexpr int kThreads = 32 * (kCtrl + 8);
-constexpr int kStages = 4;
+constexpr int kStages = 4;  // at most
 constexpr uint32_t kWait = 1u << 22;
 constexpr float kGrow = 8.f;  // powers of two a maximum may grow by before O is rescaled
 
 struct Barriers {
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t q_full[2][2], q_empty[2][2];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], drain[2];
-    uint32_t words[kStages][2];  // the block's valid states
+    // [tile][buffer of the block]
+    uint64_t s_full[2][2], s_free[2][2], p_full[2][2], o_done[2][2];
+    uint64_t drain[2];
+    uint32_t words[kStages][4];  // the block's valid states, where a mask says which
     uint32_t tmem;
     int abort;
 };
 
 template <int D>
 struct Cfg {
-    static constexpr bool kAlias = D == 64;
-    static constexpr int kCtas = D <= 64 ? 2 : 1;
-    static constexpr uint32_t kCols = D <= 64 ? 256 : 512;
-    static constexpr uint32_t kGroupCols = kCols / 2;
-    static constexpr uint32_t kP = kAlias ? 0 : 64, kO = kAlias ? 64 : 96;
-    static constexpr uint32_t kQTile = 128u * D * 2u, kKvTile = 64u * D * 2u;
-    static constexpr int kRing = D == 32 ? 4 : D == 64 ? 2 : 3;  // stages that fit beside Q
-    static constexpr uint32_t kOffKv = 4 * kQTile;        // Q [group][2], then stages of K | V
+    static constexpr int kBlock = D == 128 ? 64 : 128;  // states of a block
+    static constexpr int kBufs = D == 128 ? 2 : 1;      // of S and P
+    static constexpr bool kAlias = D == 128;            // P in its S's columns
+    static constexpr uint32_t kCols = 512;
+    static constexpr uint32_t kGroupCols = 256;
+    // buffer x: S at x * 64, P at kP + x * 64; O
+    static constexpr uint32_t kP = kAlias ? 0 : 128, kO = kAlias ? 128 : 192;
+    static constexpr uint32_t kQTile = 128u * D * 2u, kKvTile = (uint32_t)kBlock * D * 2u;
+    static constexpr int kRing = D == 128 ? 3 : 4;  // stages that fit beside Q
+    static constexpr uint32_t kOffKv = 4 * kQTile;  // Q [group][2], then stages of K | V
     static constexpr uint32_t kOffBar = kOffKv + (uint32_t)kRing * 2u * kKvTile;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
 };
@@ -74,11 +84,11 @@ __device__ __forceinline__ uint64_t k_major(uint32_t tile, int kk, int rows) {
     if constexpr (D == 32) return ptx::smem_desc(tile + kk * 32, 16, 512, ptx::kSwizzle64B);
     return ptx::smem_desc(tile + (uint32_t)((kk >> 2) * rows * 128 + (kk & 3) * 32), 16, 1024, ptx::kSwizzle128B);
 }
-// Descriptor of V (64 states x D, channels the N axis) at its k-th 16 states.
+// Descriptor of V (rows x D, channels the N axis) at its k-th 16 states.
 template <int D>
-__device__ __forceinline__ uint64_t v_operand(uint32_t tile, int kk) {
+__device__ __forceinline__ uint64_t v_operand(uint32_t tile, int kk, int rows) {
     if constexpr (D == 32) return ptx::smem_desc(tile + kk * 1024, 16, 512, ptx::kSwizzle64B);
-    return ptx::smem_desc(tile + kk * 2048, 64 * 128, 1024, ptx::kSwizzle128B);
+    return ptx::smem_desc(tile + kk * 2048, rows * 128, 1024, ptx::kSwizzle128B);
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Barriers* sb, int* status) {
@@ -93,6 +103,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Ba
 
 // The same for a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Barriers* sb, int* status) {
+    if (__all_sync(0xffffffffu, ptx::mbar_test(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, sb, status));
 }
 
@@ -100,12 +111,14 @@ struct TcPlan {
     int pairs;    // units of 256 rows in a (entry, state head)
     int splits;
     int units;
+    int tma_q, tma_kv;  // loads by TMA (a map could be made)
 };
 
 struct Unit {
     int b, j, row0, split, n, t0, nb;  // first block and number of blocks
 };
 
+template <int BN>
 __device__ __forceinline__ Unit unit_at(const CrossGeom& g, const TcPlan& p, int u) {
     Unit x;
     x.row0 = (u % p.pairs) * 256;
@@ -115,22 +128,24 @@ __device__ __forceinline__ Unit unit_at(const CrossGeom& g, const TcPlan& p, int
     x.j = u % g.kv_heads;
     x.b = u / g.kv_heads;
     x.n = cross_len(g, x.b);
-    const int all = (x.n + 63) / 64, per = (all + p.splits - 1) / p.splits;
+    const int all = (x.n + BN - 1) / BN, per = (all + p.splits - 1) / p.splits;
     x.t0 = x.split * per;
     x.nb = max(0, min(all, x.t0 + per) - x.t0);
     return x;
 }
 
 // Columns of scores that block t has: its states, in steps of 16.
-__device__ __forceinline__ int block_cols(int n, int t) { return (min(64, n - t * 64) + 15) & ~15; }
+template <int BN>
+__device__ __forceinline__ int block_cols(int n, int t) { return (min(BN, n - t * BN) + 15) & ~15; }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
-bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+__global__ void __launch_bounds__(kThreads, 1)
+bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                     const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
                     CrossParts parts, CrossGeom g, TcPlan p, int* status) {
     using C = Cfg<D>;
-    constexpr int kRing = C::kRing;
+    constexpr int kRing = C::kRing, BN = C::kBlock, NB = C::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = ptx::smem_addr(smem);
@@ -139,18 +154,18 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
-            ptx::mbar_init(&sb->kv_full[i], 32);
+            ptx::mbar_init(&sb->kv_full[i], 1);
             ptx::mbar_init(&sb->kv_empty[i], 2);
         }
         for (int x = 0; x < 2; ++x) {
             for (int y = 0; y < 2; ++y) {
-                ptx::mbar_init(&sb->q_full[x][y], 32);
+                ptx::mbar_init(&sb->q_full[x][y], 1);
                 ptx::mbar_init(&sb->q_empty[x][y], 1);
+                ptx::mbar_init(&sb->s_full[x][y], 1);
+                ptx::mbar_init(&sb->s_free[x][y], 128);
+                ptx::mbar_init(&sb->p_full[x][y], 128);
+                ptx::mbar_init(&sb->o_done[x][y], 1);
             }
-            ptx::mbar_init(&sb->s_full[x], 1);
-            ptx::mbar_init(&sb->s_free[x], 128);
-            ptx::mbar_init(&sb->p_full[x], 128);
-            ptx::mbar_init(&sb->o_done[x], 1);
             ptx::mbar_init(&sb->drain[x], 1);
         }
         sb->abort = 0;
@@ -172,50 +187,47 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
             const int grp = warp;
             const uint32_t cols = tmem + (uint32_t)grp * C::kGroupCols;
             const uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
-            int kb = 0, use = 0;  // blocks and tiles so far
+            int i = 0, use = 0;  // blocks and tiles so far
             bool ok = true;
-            auto pv = [&](const Unit& x, int b, int kk0) -> bool {  // O += P V of block b, the tile's kk0-th in all
-                const int stage = kk0 % kRing;
-                if (!wait_or_abort(&sb->p_full[grp], kk0 & 1, sb, status)) return false;
+            // S = Q K^T of block ``at`` (the tile's b-th)
+            auto qk = [&](const Unit& x, int b, int at) -> bool {
+                const int stage = at % kRing, buf = at % NB;
+                if (!wait_or_abort(&sb->kv_full[stage], (at / kRing) & 1, sb, status)) return false;
+                // the buffer's last S: read, or (P shares its columns) used by its P V
+                if (at >= NB && !wait_or_abort(C::kAlias ? &sb->o_done[grp][buf] : &sb->s_free[grp][buf],
+                                               (at / NB - 1) & 1, sb, status))
+                    return false;
+                ptx::tc_fence_after();
+                const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
+                const uint32_t kt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile;
+                const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<BN>(x.n, x.t0 + b), false, false);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_bf16(cols + (uint32_t)buf * 64u, k_major<D>(qt, kk, 128), k_major<D>(kt, kk, BN), idesc, kk);
+                ptx::mma_commit(&sb->s_full[grp][buf]);
+                if (b == x.nb - 1) ptx::mma_commit(&sb->q_empty[grp][use & 1]);
+                return true;
+            };
+            // O += P V
+            auto pv = [&](const Unit& x, int b, int at) -> bool {
+                const int stage = at % kRing, buf = at % NB;
+                if (!wait_or_abort(&sb->p_full[grp][buf], (at / NB) & 1, sb, status)) return false;
                 ptx::tc_fence_after();
                 const uint32_t vt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile;
-                const int steps = block_cols(x.n, x.t0 + b) >> 4;
+                const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
                 for (int kk = 0; kk < steps; ++kk)
-                    ptx::mma_bf16_ta(cols + C::kO, cols + C::kP + (uint32_t)kk * 8u, v_operand<D>(vt, kk), idesc_o,
-                                     b > 0 || kk > 0);
-                ptx::mma_commit(&sb->o_done[grp]);
+                    ptx::mma_bf16_ta(cols + C::kO, cols + C::kP + (uint32_t)buf * 64u + (uint32_t)kk * 8u,
+                                     v_operand<D>(vt, kk, BN), idesc_o, b > 0 || kk > 0);
+                ptx::mma_commit(&sb->o_done[grp][buf]);
                 ptx::mma_commit(&sb->kv_empty[stage]);
                 return true;
             };
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const Unit x = unit_at(g, p, u);
+                const Unit x = unit_at<BN>(g, p, u);
                 if (x.nb == 0) continue;
-                ok = wait_or_abort(&sb->q_full[grp][use & 1], (use >> 1) & 1, sb, status);
-                const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
-                for (int b = 0; ok && b < x.nb; ++b) {
-                    const int i = kb + b, stage = i % kRing;
-                    if (!wait_or_abort(&sb->kv_full[stage], (i / kRing) & 1, sb, status) ||
-                        (i > 0 && !wait_or_abort(C::kAlias ? &sb->o_done[grp] : &sb->s_free[grp], (i - 1) & 1, sb,
-                                                 status))) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t kt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile;
-                    const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols(x.n, x.t0 + b), false, false);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::mma_bf16(cols, k_major<D>(qt, kk, 128), k_major<D>(kt, kk, 64), idesc, kk);
-                    ptx::mma_commit(&sb->s_full[grp]);
-                    if (b == x.nb - 1) ptx::mma_commit(&sb->q_empty[grp][use & 1]);
-                    if constexpr (C::kAlias) {
-                        ok = pv(x, b, i);
-                    } else {
-                        if (b > 0) ok = pv(x, b - 1, i - 1);
-                    }
-                }
-                if (!C::kAlias && ok) ok = pv(x, x.nb - 1, kb + x.nb - 1);
-                kb += x.nb;
+                ok = wait_or_abort(&sb->q_full[grp][use & 1], (use >> 1) & 1, sb, status) && qk(x, 0, i);
+                for (int b = 0; ok && b < x.nb; ++b) ok = (b + 1 == x.nb || qk(x, b + 1, i + b + 1)) && pv(x, b, i + b);
+                i += x.nb;
                 ++use;
             }
             ptx::mma_commit(&sb->drain[grp]);
@@ -224,63 +236,102 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
         __syncwarp();
     } else if (warp < kCtrl) {
         // ------------------------------------------------------------------ loads
-        const int grp = warp - 2;
-        int kb = 0, use = 0;
+        constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
+        if (lane == 0) {
+            ptx::tma_prefetch_desc(&tq);
+            ptx::tma_prefetch_desc(&tk);
+            ptx::tma_prefetch_desc(&tv);
+        }
+        int i = 0, use = 0;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at(g, p, u);
+            const Unit x = unit_at<BN>(g, p, u);
             if (x.nb == 0) continue;
-            if (use >= 2 && !warp_wait(&sb->q_empty[grp][use & 1], ((use >> 1) - 1) & 1, sb, status)) break;
-            {
+            for (int grp = 0; grp < 2; ++grp) {
+                uint64_t* full = &sb->q_full[grp][use & 1];
+                if (use >= 2 && !warp_wait(&sb->q_empty[grp][use & 1], ((use >> 1) - 1) & 1, sb, status)) {
+                    ok = false;
+                    break;
+                }
                 const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
                 const int row0 = x.row0 + grp * 128;
+                if (p.tma_q) {
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(full, C::kQTile);
+#pragma unroll
+                        for (int c = 0; c < kPanels; ++c)
+                            ptx::tma_load_4d(qt + (uint32_t)c * 128u * 128u, &tq, c * 64, x.j * g.rep, row0 / g.rep,
+                                             g.q_batch ? x.b : 0, full);
+                    }
+                } else {
 #pragma unroll 4
-                for (int e = lane; e < 128 * (D / 8); e += 32) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const bool on = row0 + r < g.rows;
-                    ptx::cp_async16_zfill(qt + op_offset<D>(r, c, 128),
-                                          on ? q + cross_q_offset(g, x.b, x.j, row0 + r) + c * 8 : q, on ? 16u : 0u);
+                    for (int e = lane; e < 128 * (D / 8); e += 32) {
+                        const int r = e / (D / 8), c = e % (D / 8);
+                        const bool on = row0 + r < g.rows;
+                        ptx::cp_async16_zfill(qt + op_offset<D>(r, c, 128),
+                                              on ? q + cross_q_offset(g, x.b, x.j, row0 + r) + c * 8 : q,
+                                              on ? 16u : 0u);
+                    }
+                    ptx::cp_async_wait_all();
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(full);
                 }
-                ptx::cp_async_wait_all();
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&sb->q_full[grp][use & 1]);
             }
             const __nv_bfloat16* kbase = k + (size_t)x.b * g.k_batch + (size_t)x.j * D;
             const __nv_bfloat16* vbase = v + (size_t)x.b * g.v_batch + (size_t)x.j * D;
-            for (int b = 0; b < x.nb; ++b) {
-                const int i = kb + b, stage = i % kRing;
-                if ((i & 1) != grp) continue;  // the other loader's block
-                const int key0 = (x.t0 + b) * 64;
-                uint32_t w[2];
+            for (int b = 0; ok && b < x.nb; ++b, ++i) {
+                const int stage = i % kRing, key0 = (x.t0 + b) * BN;
+                uint32_t w[BN / 32], every = 0xffffffffu;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < BN / 32; ++h) {
                     const int key = key0 + h * 32 + lane;
                     w[h] = __ballot_sync(0xffffffffu,
                                          key < x.n && (!g.kv_mask || __ldcg(g.kv_mask + (size_t)x.b * g.Lk + key) != 0));
+                    every &= w[h];
                 }
                 if (i >= kRing && !warp_wait(&sb->kv_empty[stage], ((i / kRing) - 1) & 1, sb, status)) {
                     ok = false;
                     break;
                 }
                 const uint32_t kt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile;
+                uint64_t* full = &sb->kv_full[stage];
+                if (lane == 0 && g.kv_mask) {
+#pragma unroll
+                    for (int h = 0; h < BN / 32; ++h) sb->words[stage][h] = w[h];
+                }
+                if (p.tma_kv && every == 0xffffffffu) {
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(full, 2u * C::kKvTile);
+#pragma unroll
+                        for (int c = 0; c < kPanels; ++c) {
+                            ptx::tma_load_4d(kt + (uint32_t)c * BN * 128u, &tk, c * 64, x.j, key0, g.k_batch ? x.b : 0,
+                                             full);
+                            ptx::tma_load_4d(kt + C::kKvTile + (uint32_t)c * BN * 128u, &tv, c * 64, x.j, key0,
+                                             g.v_batch ? x.b : 0, full);
+                        }
+                    }
+                } else {
+                    const int rows = block_cols<BN>(x.n, x.t0 + b);  // no product reads past them
 #pragma unroll 4
-                for (int e = lane; e < 64 * (D / 8); e += 32) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const bool on = ((r < 32 ? w[0] : w[1]) >> (r & 31)) & 1u;
-                    const uint32_t at = op_offset<D>(r, c, 64);
-                    ptx::cp_async16_zfill(kt + at, on ? kbase + (size_t)(key0 + r) * g.k_row + c * 8 : k, on ? 16u : 0u);
-                    ptx::cp_async16_zfill(kt + C::kKvTile + at, on ? vbase + (size_t)(key0 + r) * g.v_row + c * 8 : v,
-                                          on ? 16u : 0u);
+                    for (int e = lane; e < rows * (D / 8); e += 32) {
+                        const int r = e / (D / 8), c = e % (D / 8);
+                        uint32_t word = w[0];
+#pragma unroll
+                        for (int h = 1; h < BN / 32; ++h) word = r >= h * 32 ? w[h] : word;
+                        const bool on = (word >> (r & 31)) & 1u;
+                        const uint32_t at = op_offset<D>(r, c, BN);
+                        ptx::cp_async16_zfill(kt + at, on ? kbase + (size_t)(key0 + r) * g.k_row + c * 8 : k,
+                                              on ? 16u : 0u);
+                        ptx::cp_async16_zfill(kt + C::kKvTile + at,
+                                              on ? vbase + (size_t)(key0 + r) * g.v_row + c * 8 : v, on ? 16u : 0u);
+                    }
+                    ptx::cp_async_wait_all();
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(full);
                 }
-                if (lane == 0) {
-                    sb->words[stage][0] = w[0];
-                    sb->words[stage][1] = w[1];
-                }
-                ptx::cp_async_wait_all();
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&sb->kv_full[stage]);
             }
-            kb += x.nb;
             ++use;
         }
     } else {
@@ -293,50 +344,66 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
         int i = 0;  // blocks so far
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at(g, p, u);
+            const Unit x = unit_at<BN>(g, p, u);
             float m = -INFINITY;
             uint64_t l2 = 0ull;
             for (int b = 0; b < x.nb; ++b, ++i) {
-                const int stage = i % kRing;
-                if (!warp_wait(&sb->kv_full[stage], (i / kRing) & 1, sb, status) ||
-                    !warp_wait(&sb->s_full[grp], i & 1, sb, status)) {
+                const int buf = i % NB, phase = i / NB;
+                const uint32_t scol = cols + (uint32_t)buf * 64u;
+                if (!warp_wait(&sb->s_full[grp][buf], phase & 1, sb, status)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t w0 = sb->words[stage][0], w1 = sb->words[stage][1];
-                const int nc = block_cols(x.n, x.t0 + b);
-                const bool whole = (w0 & w1) == 0xffffffffu;
-                float mx[2] = {-INFINITY, -INFINITY};
+                // the row's scores; columns that no product wrote are masked below
+                const int nc = block_cols<BN>(x.n, x.t0 + b);
+                uint32_t r[BN / 32][32];
+                ptx::tmem_load(scol, r);
+                if constexpr (!C::kAlias) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&sb->s_free[grp][buf]);
+                }
+                const int left = x.n - (x.t0 + b) * BN;
+                if (g.kv_mask || left < BN) {
+                    // (the block's loads are done; the wait makes the loader's words visible)
+                    if (g.kv_mask && !warp_wait(&sb->kv_full[i % kRing], (i / kRing) & 1, sb, status)) {
+                        ok = false;
+                        break;
+                    }
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    if (c >= nc) break;
-                    uint32_t r[2][16];
-                    ptx::tmem_ld16(cols + c, r[0]);
-                    ptx::tmem_ld16(cols + c + 16, r[1]);
-                    ptx::tmem_wait16(r[0]);
-                    ptx::tmem_wait16(r[1]);
-                    if (whole) {
+                    for (int h = 0; h < BN / 32; ++h) {
+                        const int rest = left - h * 32;
+                        const uint32_t w = g.kv_mask ? sb->words[i % kRing][h]
+                                                     : (rest >= 32 ? 0xffffffffu : rest <= 0 ? 0u : (1u << rest) - 1u);
+                        if (w != 0xffffffffu) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            mx[e & 1] = fmaxf(mx[e & 1], fmaxf(__uint_as_float(r[0][e]), __uint_as_float(r[1][e])));
-                    } else {
-                        const uint32_t w = c == 0 ? w0 : w1;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((w >> e) & 1u) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(r[e >> 4][e & 15]));
+                            for (int e = 0; e < 32; ++e)
+                                if (!((w >> e) & 1u)) r[h][e] = 0xff800000u;  // -inf
+                        }
                     }
                 }
-                const float mn = fmaxf(mx[0], mx[1]) * sl;
-                // the previous block's P V: its P is overwritten below, its O may be rescaled
-                if (i > 0 && !warp_wait(&sb->o_done[grp], (i - 1) & 1, sb, status)) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int h = 0; h < BN / 32; ++h)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        mx[(e >> 1) & 3] =
+                            ptx::max3(mx[(e >> 1) & 3], __uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1]));
+                const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+                // P's buffer: its last P V is done
+                if (i >= NB && !warp_wait(&sb->o_done[grp][buf], (phase - 1) & 1, sb, status)) {
                     ok = false;
                     break;
                 }
-                ptx::tc_fence_after();
                 if (b == 0) {
                     m = mn;
                 } else if (__any_sync(0xffffffffu, mn > m + kGrow)) {
+                    // O stands still once the previous block's P V is done
+                    if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, sb, status)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
                     const float to = mn > m + kGrow ? mn : m;
                     const float alpha = to == -INFINITY ? 1.f : ptx::ex2(m - to);
                     m = to;
@@ -353,25 +420,17 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
                         ptx::tmem_st16(cols + C::kO + c, r);
                     }
                 }
+                ptx::tc_fence_after();
                 const float mu = m == -INFINITY ? 0.f : m;  // no valid state yet
                 const uint64_t neg = ptx::pack_f32x2(-mu, -mu);
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    if (c >= nc) break;
-                    uint32_t r[16], pk[8];
-                    ptx::tmem_ld16(cols + c, r);
-                    ptx::tmem_wait16(r);
-                    if (!whole) {
-                        const uint32_t w = (c < 32 ? w0 : w1) >> (c & 31);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (!((w >> e) & 1u)) r[e] = 0xff800000u;  // -inf
-                    }
+                // P = 2^(s - m) of 16 columns, rounded once to bf16 for the product
+                auto chunk = [&](const uint32_t* sc, uint32_t col) {
+                    uint32_t pk[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         float lo, hi;
-                        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(r[2 * e]),
-                                                                         __uint_as_float(r[2 * e + 1])),
+                        ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(sc[2 * e]),
+                                                                         __uint_as_float(sc[2 * e + 1])),
                                                          sl2, neg),
                                           lo, hi);
                         lo = ptx::ex2(lo);
@@ -379,17 +438,23 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
                         l2 = ptx::add_f32x2(l2, ptx::pack_f32x2(lo, hi));
                         pk[e] = ptx::pack_bf16x2(lo, hi);
                     }
-                    // d = 64: P overwrites scores that this thread has read (chunks 0.. of S hold P's chunks 0..)
-                    ptx::tmem_st8(cols + C::kP + c / 2, pk);
+                    ptx::tmem_st8(cols + C::kP + (uint32_t)buf * 64u + col / 2, pk);
+                };
+                if (nc == BN) {  // without branches the exponentials of the chunks overlap
+#pragma unroll
+                    for (int h = 0; h < BN / 16; ++h) chunk(r[h >> 1] + (h & 1) * 16, h * 16);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < BN / 16; ++h)
+                        if (nc > h * 16) chunk(r[h >> 1] + (h & 1) * 16, h * 16);
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
-                if constexpr (!C::kAlias) ptx::mbar_arrive(&sb->s_free[grp]);
-                ptx::mbar_arrive(&sb->p_full[grp]);
+                ptx::mbar_arrive(&sb->p_full[grp][buf]);
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->o_done[grp], (i - 1) & 1, sb, status)) break;
+                if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, sb, status)) break;
                 ptx::tc_fence_after();
             }
             float lo, hi;
@@ -442,14 +507,21 @@ bra_cross_tc_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
 }
 
 template <int D>
-bra_status launch_d(const CrossGeom& g, const TcPlan& p, int grid, const void* q, const void* k, const void* v,
+bra_status launch_d(const CrossGeom& g, const TcPlan& plan, int grid, const void* q, const void* k, const void* v,
                     void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream) {
     using C = Cfg<D>;
     if (cudaFuncSetAttribute(bra_cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
         cudaSuccess)
         return BRA_ERR_CUDA;
+    TcPlan p = plan;
+    CUtensorMap tq = {}, tk = {}, tv = {};
+    // a Q tile is 128 / rep tokens; where rep does not divide it, and where a step is too long, cp.async
+    p.tma_q = 128 % g.rep == 0 && encode_heads_map(&tq, q, g.B, g.Lq, g.heads, D, g.q_row, g.q_batch, 128 / g.rep, g.rep);
+    p.tma_kv = g.Lk >= C::kBlock && encode_heads_map(&tk, k, g.B, g.Lk, g.kv_heads, D, g.k_row, g.k_batch, C::kBlock, 1) &&
+               encode_heads_map(&tv, v, g.B, g.Lk, g.kv_heads, D, g.v_row, g.v_batch, C::kBlock, 1);
     const cudaError_t e = launch_after_previous(
-        bra_cross_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kSmem, stream, static_cast<const __nv_bfloat16*>(q),
+        bra_cross_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv,
+        static_cast<const __nv_bfloat16*>(q),
         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o),
         lse, parts, g, p, status);
     return e == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
@@ -463,7 +535,7 @@ int cross_tc_rows() { return 256; }
 
 bra_status cross_forward_tc(const CrossGeom& g, int splits, const void* q, const void* k, const void* v, void* o,
                             float* lse, CrossParts parts, int* status, cudaStream_t stream) {
-    TcPlan p;
+    TcPlan p = {};
     p.pairs = (g.rows + 255) / 256;
     p.splits = splits;
     const long long units = (long long)p.pairs * splits * g.kv_heads * g.B;
@@ -471,7 +543,7 @@ bra_status cross_forward_tc(const CrossGeom& g, int splits, const void* q, const
     p.units = (int)units;
     const int sms = sm_count();
     if (sms <= 0) return BRA_ERR_CUDA;
-    const long long most = (long long)sms * (g.d <= 64 ? 2 : 1);
+    const long long most = sms;
     const int grid = units < most ? (int)units : (int)most;
     return g.d == 32   ? launch_d<32>(g, p, grid, q, k, v, o, lse, parts, status, stream)
            : g.d == 64 ? launch_d<64>(g, p, grid, q, k, v, o, lse, parts, status, stream)

@@ -288,34 +288,50 @@ def _token_strides(t, name: str, width: int):
     return B, L, row, sb if B > 1 else L * row
 
 
-def _same_tokens(t, name, width, B, L, row, batch, dtype, device):
+def _same_tokens(t, name, width, B, L, row, batch, dtype, dev: int):
     """``t`` is what the shape says: its size, steps, type and device."""
-    if _dtype_code(t) != dtype or t.device != device:
-        raise ValueError(f"{name}: expected the shape's type on {device}, got {t.dtype} on {t.device}")
-    if _token_strides(t, name, width) != (B, L, row, batch):
-        raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} is not what the shape says")
+    if t.dtype is dtype and t.get_device() == dev:
+        if t.dim() == 3:
+            size, step = t.shape, t.stride()
+            if (size[0] == B and size[1] == L and size[2] == width and step[2] == 1 and (L <= 1 or step[1] == row)
+                    and (B <= 1 or step[0] == batch)):
+                return
+        elif _token_strides(t, name, width) == (B, L, row, batch):
+            return
+    raise ValueError(f"{name}: {t.dtype} of {tuple(t.shape)}, strides {t.stride()}, on {t.device} is not what the "
+                     f"shape says ({dtype} of [{B}, {L}, {width}], steps {batch}, {row}, on cuda:{dev})")
 
 
-def _dense(t, name, dtype, numel, device):
-    if t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on {device}")
+def _dense(t, name, dtype, numel, dev: int):
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on cuda:{dev}, got "
+                         f"{t.dtype} of {tuple(t.shape)} on {t.device}")
 
 
-def _call(where: str, fn, device, stream, *args):
-    """``fn(*args, stream)`` with ``device`` current; None is its current stream."""
+def _cuda_device(t, where: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{where}: expected CUDA tensors, got one on {t.device}")
+    return t.get_device()
+
+
+def _call(where: str, fn, dev: int, stream, *args):
+    """``fn(*args, stream)`` with device ``dev`` current; None is its current stream."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"{where}: expected CUDA tensors, got {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(dev)
     raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             status = fn(*args, raw)
     if status != BRA_OK:
         raise BraError(status, where)
+
+
+def _torch_dtype(code: int):
+    import torch
+    return torch.bfloat16 if code == BRA_DTYPE_BF16 else torch.float32
 
 
 def cross_shape_for(q, k, v, heads: int, kv_heads: int | None = None, scale: float | None = None) -> BraCrossShape:
@@ -339,10 +355,11 @@ def cross_shape_for(q, k, v, heads: int, kv_heads: int | None = None, scale: flo
 
 def _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace):
     import torch
-    dev = q.device
-    _same_tokens(q, "q", s.heads * s.d, s.B, s.Lq, s.q_row, s.q_batch, s.dtype, dev)
-    _same_tokens(k, "k", s.kv_heads * s.d, s.B, s.Lk, s.k_row, s.k_batch, s.dtype, dev)
-    _same_tokens(v, "v", s.kv_heads * s.d, s.B, s.Lk, s.v_row, s.v_batch, s.dtype, dev)
+    dev, dtype = _cuda_device(q, "cross attention"), _torch_dtype(s.dtype)
+    B, Lk, wk = s.B, s.Lk, s.kv_heads * s.d
+    _same_tokens(q, "q", s.heads * s.d, B, s.Lq, s.q_row, s.q_batch, dtype, dev)
+    _same_tokens(k, "k", wk, B, Lk, s.k_row, s.k_batch, dtype, dev)
+    _same_tokens(v, "v", wk, B, Lk, s.v_row, s.v_batch, dtype, dev)
     if kv_len is not None:
         _dense(kv_len, "kv_len", torch.int32, s.B, dev)
     if kv_mask is not None:
@@ -449,17 +466,18 @@ def bra_rotary(shape: BraRotaryShape, q, k, pos, inv_freq, q_out, k_out, stream=
     (time, height, width), or None for the shape's grid; inv_freq fp32, one for
     each pair.  k and k_out may both be None."""
     import torch
-    s, dev = shape, q.device
+    s, dev = shape, _cuda_device(q, "rotary positions")
+    dtype, B = _torch_dtype(s.dtype), s.B
     L, wq, wk = s.T * s.H * s.W, s.heads * s.d, s.kv_heads * s.d
-    _same_tokens(q, "q", wq, s.B, L, s.q_row, s.q_batch, s.dtype, dev)
-    _same_tokens(q_out, "q_out", wq, s.B, L, s.qo_row, s.qo_batch, s.dtype, dev)
+    _same_tokens(q, "q", wq, B, L, s.q_row, s.q_batch, dtype, dev)
+    _same_tokens(q_out, "q_out", wq, B, L, s.qo_row, s.qo_batch, dtype, dev)
     if (k is None) != (k_out is None) or (k is None) != (s.kv_heads == 0):
         raise ValueError("k, k_out and the shape's kv_heads go together")
     if k is not None:
-        _same_tokens(k, "k", wk, s.B, L, s.k_row, s.k_batch, s.dtype, dev)
-        _same_tokens(k_out, "k_out", wk, s.B, L, s.ko_row, s.ko_batch, s.dtype, dev)
+        _same_tokens(k, "k", wk, B, L, s.k_row, s.k_batch, dtype, dev)
+        _same_tokens(k_out, "k_out", wk, B, L, s.ko_row, s.ko_batch, dtype, dev)
     if pos is not None:
-        _dense(pos, "pos", torch.int32, (s.B - 1) * s.pos_batch + L * 3 if s.B else 0, dev)
+        _dense(pos, "pos", torch.int32, (B - 1) * s.pos_batch + L * 3 if B else 0, dev)
     _dense(inv_freq, "inv_freq", torch.float32, sum(s.pairs), dev)
     _call("bra_rotary", _lib.bra_rotary, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(pos), _ptr(inv_freq),
           _ptr(q_out), _ptr(k_out))
@@ -471,7 +489,7 @@ def bra_dropout_add(x, residual, p: float, rng, y, unit: int = 1, stream=None) -
     (or uint64) tensor {seed, offset} on x's device.  The gradient of x is the
     same call on the gradient of y, without a residual."""
     import torch
-    n, dev = x.numel(), x.device
+    n, dev = x.numel(), _cuda_device(x, "dropout")
     dtype = _dtype_code(x)
     for t, name in ((x, "x"), (residual, "residual"), (y, "y")):
         if t is not None:

@@ -9,7 +9,8 @@
 // read from device memory, so that a replayed graph can be given new ones.
 //
 // Bound by HBM (x and the residual read, y written); the ten rounds cost
-// about 15 instructions an element, below the rate of the loads.
+// about 15 instructions an element, below the rate of the loads.  A thread has
+// kVectors vectors of eight elements in flight (DROPOUT_NOTE).
 #include "kernels.h"
 #include "rotary.h"
 #include "tma_host.h"
@@ -18,6 +19,7 @@ namespace bra {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kVectors = 4;
 
 __device__ __forceinline__ uint4 philox(uint64_t seed, uint64_t counter) {
     uint32_t x0 = (uint32_t)counter, x1 = (uint32_t)(counter >> 32), x2 = 0u, x3 = 0u;
@@ -49,59 +51,68 @@ __device__ __forceinline__ void one(int64_t i, int64_t unit, uint64_t threshold,
     y[i] = from_f32<T>(keep ? fmaf(to_f32(x[i]), scale, r) : r);
 }
 
-// Thread = eight consecutive elements (two counters; or one draw, where a
-// unit is a multiple of eight).
+// A vector is eight consecutive elements (two counters; or one draw, where a
+// unit is a multiple of eight); a CTA's are consecutive, a thread's kThreads apart.
 template <typename T, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 bra_dropout_add_kernel(const T* x, const T* residual, T* y, int64_t n, int64_t unit, uint64_t threshold, float scale,
                        const uint64_t* rng) {
-    constexpr int kVecs = sizeof(T) == 2 ? 1 : 2;  // 16-byte vectors of eight elements
+    constexpr int kWords = sizeof(T) == 2 ? 1 : 2;  // 16-byte words of eight elements
     grid_dependency_wait();
-    const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (at >= n) return;
-    const uint64_t seed = __ldcg(reinterpret_cast<const unsigned long long*>(rng));
-    const uint64_t offset = __ldcg(reinterpret_cast<const unsigned long long*>(rng) + 1);
-    if (at + 8 > n) {
-        for (int64_t i = at; i < n; ++i) one<T>(i, unit, threshold, scale, seed, offset, x, residual, y);
-        return;
-    }
-    uint4 xv[kVecs], rv[kVecs];
+    const int64_t first = ((int64_t)blockIdx.x * kVectors * kThreads + threadIdx.x) * 8;
+    uint4 xv[kVectors][kWords], rv[kVectors][kWords];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        xv[i] = *(reinterpret_cast<const uint4*>(x + at) + i);
-        rv[i] = residual ? *(reinterpret_cast<const uint4*>(residual + at) + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    bool keep[8];
-    if constexpr (SHARED) {
-        const uint64_t u = (uint64_t)(at / unit);
-        const bool on = word_of(philox(seed, offset + u / 4), (int)(u & 3)) >= threshold;
+    for (int j = 0; j < kVectors; ++j) {
+        const int64_t at = first + (int64_t)j * kThreads * 8;
+        if (at + 8 > n) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) keep[i] = on;
-    } else {
-        const uint64_t c = offset + (uint64_t)at / 4;
-        const uint4 a = philox(seed, c), b = philox(seed, c + 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            keep[i] = word_of(a, i) >= threshold;
-            keep[4 + i] = word_of(b, i) >= threshold;
+        for (int i = 0; i < kWords; ++i) {
+            xv[j][i] = *(reinterpret_cast<const uint4*>(x + at) + i);
+            rv[j][i] = residual ? *(reinterpret_cast<const uint4*>(residual + at) + i) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    float f[8], r[8];
+    const uint64_t seed = __ldcg(reinterpret_cast<const unsigned long long*>(rng));
+    const uint64_t offset = __ldcg(reinterpret_cast<const unsigned long long*>(rng) + 1);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        unpack16(xv[i], f + i * (8 / kVecs), (const T*)nullptr);
-        unpack16(rv[i], r + i * (8 / kVecs), (const T*)nullptr);
-    }
+    for (int j = 0; j < kVectors; ++j) {
+        const int64_t at = first + (int64_t)j * kThreads * 8;
+        if (at >= n) break;
+        if (at + 8 > n) {
+            for (int64_t i = at; i < n; ++i) one<T>(i, unit, threshold, scale, seed, offset, x, residual, y);
+            break;
+        }
+        bool keep[8];
+        if constexpr (SHARED) {
+            const uint64_t u = (uint64_t)(at / unit);
+            const bool on = word_of(philox(seed, offset + u / 4), (int)(u & 3)) >= threshold;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = keep[i] ? fmaf(f[i], scale, r[i]) : r[i];
-    if constexpr (sizeof(T) == 2) {
-        __nv_bfloat162 h[4];
+            for (int i = 0; i < 8; ++i) keep[i] = on;
+        } else {
+            const uint64_t c = offset + (uint64_t)at / 4;
+            const uint4 a = philox(seed, c), b = philox(seed, c + 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        *reinterpret_cast<uint4*>(y + at) = *reinterpret_cast<uint4*>(h);
-    } else {
-        *reinterpret_cast<float4*>(y + at) = make_float4(f[0], f[1], f[2], f[3]);
-        *(reinterpret_cast<float4*>(y + at) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+            for (int i = 0; i < 4; ++i) {
+                keep[i] = word_of(a, i) >= threshold;
+                keep[4 + i] = word_of(b, i) >= threshold;
+            }
+        }
+        float f[8], r[8];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            unpack16(xv[j][i], f + i * (8 / kWords), (const T*)nullptr);
+            unpack16(rv[j][i], r + i * (8 / kWords), (const T*)nullptr);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = keep[i] ? fmaf(f[i], scale, r[i]) : r[i];
+        if constexpr (sizeof(T) == 2) {
+            __nv_bfloat162 h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            *reinterpret_cast<uint4*>(y + at) = *reinterpret_cast<uint4*>(h);
+        } else {
+            *reinterpret_cast<float4*>(y + at) = make_float4(f[0], f[1], f[2], f[3]);
+            *(reinterpret_cast<float4*>(y + at) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+        }
     }
     allow_dependents();
 }
@@ -109,7 +120,7 @@ bra_dropout_add_kernel(const T* x, const T* residual, T* y, int64_t n, int64_t u
 template <typename T>
 cudaError_t launch(int64_t n, int64_t unit, uint64_t threshold, float scale, const uint64_t* rng, const void* x,
                    const void* residual, void* y, cudaStream_t stream) {
-    const int64_t grid = ((n + 7) / 8 + kThreads - 1) / kThreads;
+    const int64_t grid = ((n + 7) / 8 + kVectors * kThreads - 1) / (kVectors * kThreads);
     auto* kernel = unit == 1 ? bra_dropout_add_kernel<T, false> : bra_dropout_add_kernel<T, true>;
     return launch_after_previous(kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, static_cast<const T*>(x),
                                  static_cast<const T*>(residual), static_cast<T*>(y), n, unit, threshold, scale, rng);

@@ -8,8 +8,9 @@
 // of a turn), so position x frequency and its reduction to a fraction of a
 // turn are done in fp64; sine and cosine of the reduced angle in fp32.
 //
-// Bound by HBM: Q and K are read and written once, in 16-byte vectors; a
-// thread's loads are issued before the CTA's angles are formed.
+// Bound by HBM: Q and K are read and written once, in 16-byte vectors, four
+// units a thread, whose loads are issued before the CTA's angles are formed, so
+// that forming them runs under the loads (ROTARY_NOTE).
 #include "kernels.h"
 #include "rotary.h"
 #include "tma_host.h"
@@ -19,6 +20,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxAngles = 2048;  // (token, pair) angles of a CTA: 16 KB of shared memory
+constexpr int kUnits = 4;         // units of a thread
+constexpr int kMaxTokens = 256;   // of a CTA
+
+// x / d for x d < 2^32, by the multiplier floor(2^32 / d) + 1 (d > 1): a CTA's
+// counts are small, and a division by a value known at launch would cost more
+// than the rotation.
+struct Divisor {
+    uint32_t d, m;
+};
+__device__ __forceinline__ int divide(int x, Divisor v) { return v.d == 1 ? x : (int)__umulhi((uint32_t)x, v.m); }
+Divisor divisor(int d) { return {(uint32_t)d, d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d + 1) : 0u}; }
 
 // A unit of work: V channels that hold V / 2 pairs (interleaved), or V first
 // halves and their V partners P channels on (split halves), or V channels
@@ -60,28 +72,65 @@ __device__ __forceinline__ typename Vec<T, V>::type narrow(const float (&f)[V]) 
 // PAIRED: a unit is two vectors (split halves); else one (interleaved).
 template <typename T, int V, bool PAIRED>
 __global__ void __launch_bounds__(kThreads)
-bra_rotary_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_t* __restrict__ pos,
-                  const float* __restrict__ inv_freq, T* __restrict__ qo, T* __restrict__ ko, RotaryGeom g,
-                  int tokens_per_cta, int units_turn, int units_head) {
+bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_freq, T* qo, T* ko, RotaryGeom g,
+                  int tokens_per_cta, int units_turn, Divisor per_token, Divisor per_head, Divisor pairs) {
     using U = typename Vec<T, V>::type;
     __shared__ float2 table[kMaxAngles];
-    const long long tokens = (long long)g.B * g.L;
-    const long long token0 = (long long)blockIdx.x * tokens_per_cta;
-    const int here = (int)min((long long)tokens_per_cta, tokens - token0);
+    __shared__ int place[kMaxTokens][3];
+    // CTA = consecutive tokens of one entry
+    const int b = blockIdx.y, l0 = blockIdx.x * tokens_per_cta, here = min(tokens_per_cta, g.L - l0);
+    const int units = here * (int)per_token.d;
     grid_dependency_wait();
 
-    for (int e = threadIdx.x; e < here * g.P; e += kThreads) {
-        const int tk = e / g.P, i = e - tk * g.P;
-        const long long at = token0 + tk;
-        const int b = (int)(at / g.L), l = (int)(at - (long long)b * g.L);
-        const int axis = i < g.axis1 ? 0 : (i < g.axis2 ? 1 : 2);
-        int p;
-        if (pos) {
-            p = __ldcg(pos + (size_t)b * g.pos_batch + (size_t)l * 3 + axis);
-        } else {
-            const int row = l / g.W;
-            p = axis == 2 ? l - row * g.W : (axis == 1 ? row % g.H : row / g.H);
+    // the unit's channels c (and P + c), where they come from and go to
+    struct Unit {
+        const T* src;
+        T* dst;
+        int tab, c;  // first angle of the token; first channel, or -1
+        bool turn;
+        U a, z;
+    } un[kUnits];
+    auto fetch = [&](int u0) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = u0 + i * kThreads;
+            un[i].c = -1;
+            if (u >= units) continue;
+            const int tk = here > 1 ? divide(u, per_token) : 0, w = u - tk * (int)per_token.d;
+            const int head = divide(w, per_head), x = w - head * (int)per_head.d, l = l0 + tk;
+            if (head < g.heads) {
+                un[i].src = q + (size_t)b * g.q_batch + (size_t)l * g.q_row + (size_t)head * g.d;
+                un[i].dst = qo + (size_t)b * g.qo_batch + (size_t)l * g.qo_row + (size_t)head * g.d;
+            } else {
+                un[i].src = k + (size_t)b * g.k_batch + (size_t)l * g.k_row + (size_t)(head - g.heads) * g.d;
+                un[i].dst = ko + (size_t)b * g.ko_batch + (size_t)l * g.ko_row + (size_t)(head - g.heads) * g.d;
+            }
+            un[i].tab = tk * g.P;
+            un[i].turn = x < units_turn;
+            un[i].c = PAIRED && !un[i].turn ? 2 * g.P + (x - units_turn) * V : x * V;
+            un[i].a = *reinterpret_cast<const U*>(un[i].src + un[i].c);
+            if (PAIRED && un[i].turn) un[i].z = *reinterpret_cast<const U*>(un[i].src + g.P + un[i].c);
         }
+    };
+    fetch(threadIdx.x);
+
+    for (int tk = threadIdx.x; tk < here; tk += kThreads) {
+        const int l = l0 + tk;
+        if (pos) {
+#pragma unroll
+            for (int axis = 0; axis < 3; ++axis)
+                place[tk][axis] = __ldcg(pos + (size_t)b * g.pos_batch + (size_t)l * 3 + axis);
+        } else {
+            const int row = l / g.W, t = row / g.H;
+            place[tk][0] = t;
+            place[tk][1] = row - t * g.H;
+            place[tk][2] = l - row * g.W;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < here * g.P; e += kThreads) {
+        const int tk = divide(e, pairs), i = e - tk * g.P;
+        const int p = place[tk][i < g.axis1 ? 0 : (i < g.axis2 ? 1 : 2)];
         // turns, reduced to [-1/2, 1/2]
         double turns = (double)p * (double)__ldcg(inv_freq + i) * 0.15915494309189533577;
         turns -= rint(turns);
@@ -91,58 +140,41 @@ bra_rotary_kernel(const T* __restrict__ q, const T* __restrict__ k, const int32_
     }
     __syncthreads();
 
-    const int heads = g.heads + g.kv_heads, per_token = heads * units_head;
-    for (int u = threadIdx.x; u < here * per_token; u += kThreads) {
-        const int tk = u / per_token, w = u - tk * per_token, head = w / units_head, x = w - head * units_head;
-        const long long at = token0 + tk;
-        const int b = (int)(at / g.L), l = (int)(at - (long long)b * g.L);
-        const T* src;
-        T* dst;
-        if (head < g.heads) {
-            src = q + (size_t)b * g.q_batch + (size_t)l * g.q_row + (size_t)head * g.d;
-            dst = qo + (size_t)b * g.qo_batch + (size_t)l * g.qo_row + (size_t)head * g.d;
-        } else {
-            src = k + (size_t)b * g.k_batch + (size_t)l * g.k_row + (size_t)(head - g.heads) * g.d;
-            dst = ko + (size_t)b * g.ko_batch + (size_t)l * g.ko_row + (size_t)(head - g.heads) * g.d;
-        }
-        const float2* tab = table + tk * g.P;
-        if constexpr (PAIRED) {
-            if (x < units_turn) {
-                const int c = x * V;
-                const U a = *reinterpret_cast<const U*>(src + c), z = *reinterpret_cast<const U*>(src + g.P + c);
+    for (int u0 = threadIdx.x; u0 < units; u0 += kUnits * kThreads) {
+        if (u0 != (int)threadIdx.x) fetch(u0);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int c = un[i].c;
+            if (c < 0) continue;
+            const float2* tab = table + un[i].tab;
+            if (!un[i].turn) {
+                *reinterpret_cast<U*>(un[i].dst + c) = un[i].a;
+            } else if constexpr (PAIRED) {
                 float f[V], h[V];
-                widen<T, V>(a, f);
-                widen<T, V>(z, h);
+                widen<T, V>(un[i].a, f);
+                widen<T, V>(un[i].z, h);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 t = tab[c + i];
-                    const float y = f[i] * t.x - h[i] * t.y;
-                    h[i] = h[i] * t.x + f[i] * t.y;
-                    f[i] = y;
+                for (int e = 0; e < V; ++e) {
+                    const float2 t = tab[c + e];
+                    const float y = f[e] * t.x - h[e] * t.y;
+                    h[e] = h[e] * t.x + f[e] * t.y;
+                    f[e] = y;
                 }
-                *reinterpret_cast<U*>(dst + c) = narrow<T, V>(f);
-                *reinterpret_cast<U*>(dst + g.P + c) = narrow<T, V>(h);
+                *reinterpret_cast<U*>(un[i].dst + c) = narrow<T, V>(f);
+                *reinterpret_cast<U*>(un[i].dst + g.P + c) = narrow<T, V>(h);
             } else {
-                const int c = 2 * g.P + (x - units_turn) * V;
-                *reinterpret_cast<U*>(dst + c) = *reinterpret_cast<const U*>(src + c);
-            }
-        } else {
-            const int c = x * V;
-            U a = *reinterpret_cast<const U*>(src + c);
-            if (x < units_turn) {
                 float f[V];
-                widen<T, V>(a, f);
+                widen<T, V>(un[i].a, f);
 #pragma unroll
-                for (int i = 0; i < V; i += 2) {
-                    if ((c + i) / 2 >= g.P) continue;
-                    const float2 t = tab[(c + i) / 2];
-                    const float y = f[i] * t.x - f[i + 1] * t.y;
-                    f[i + 1] = f[i + 1] * t.x + f[i] * t.y;
-                    f[i] = y;
+                for (int e = 0; e < V; e += 2) {
+                    if ((c + e) / 2 >= g.P) continue;  // the last unit may hold channels past the pairs
+                    const float2 t = tab[(c + e) / 2];
+                    const float y = f[e] * t.x - f[e + 1] * t.y;
+                    f[e + 1] = f[e + 1] * t.x + f[e] * t.y;
+                    f[e] = y;
                 }
-                a = narrow<T, V>(f);
+                *reinterpret_cast<U*>(un[i].dst + c) = narrow<T, V>(f);
             }
-            *reinterpret_cast<U*>(dst + c) = a;
         }
     }
     allow_dependents();
@@ -153,15 +185,21 @@ cudaError_t launch(const RotaryGeom& g, const void* q, const void* k, const int3
                    void* q_out, void* k_out, cudaStream_t stream) {
     const int units_turn = PAIRED ? g.P / V : (2 * g.P + V - 1) / V;
     const int units_head = PAIRED ? units_turn + (g.d - 2 * g.P) / V : g.d / V;
-    int per = kMaxAngles / g.P;
-    const int want = (2 * kThreads) / ((g.heads + g.kv_heads) * units_head);  // two units a thread
-    if (per > want) per = want > 0 ? want : 1;
-    const long long tokens = (long long)g.B * g.L;
-    const long long grid = (tokens + per - 1) / per;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_after_previous(bra_rotary_kernel<T, V, PAIRED>, dim3((unsigned)grid), dim3(kThreads), 0, stream,
-                                 static_cast<const T*>(q), static_cast<const T*>(k), pos, inv_freq,
-                                 static_cast<T*>(q_out), static_cast<T*>(k_out), g, per, units_turn, units_head);
+    const int units_token = (g.heads + g.kv_heads) * units_head;
+    // tokens of a CTA: kUnits units a thread, in at least two CTAs for each SM
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const long long spread = (long long)g.B * g.L / (2LL * sms) + 1;
+    int per = kUnits * kThreads / units_token;
+    if (per > kMaxAngles / g.P) per = kMaxAngles / g.P;
+    if (per > kMaxTokens) per = kMaxTokens;
+    if (per > g.L) per = g.L;
+    if (per > spread) per = (int)spread;
+    if (per < 1) per = 1;
+    return launch_after_previous(bra_rotary_kernel<T, V, PAIRED>, dim3((unsigned)((g.L + per - 1) / per), (unsigned)g.B),
+                                 dim3(kThreads), 0, stream, static_cast<const T*>(q), static_cast<const T*>(k), pos,
+                                 inv_freq, static_cast<T*>(q_out), static_cast<T*>(k_out), g, per, units_turn,
+                                 divisor(units_token), divisor(units_head), divisor(g.P));
 }
 
 }  // namespace

@@ -76,6 +76,11 @@ int cross_backward_splits(const CrossGeom& g, bool bf16);
 bra_status cross_backward_bf16(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
                                const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
                                float* delta, float* parts, int* status, cudaStream_t stream);
+bool cross_tc_backward_covers(const CrossGeom& g);
+int cross_tc_backward_splits(const CrossGeom& g);
+bra_status cross_backward_tc(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
+                             const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
+                             float* delta, float* parts, int* status, cudaStream_t stream);
 bra_status cross_backward_f32(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
                               const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
                               float* delta, float* parts, cudaStream_t stream);

@@ -444,7 +444,7 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 
 // Enough row splits for two CTAs on each SM, each of at least four row tiles.
 int cross_backward_splits(const CrossGeom& g, bool bf16) {
-    (void)bf16;
+    if (bf16 && cross_tc_backward_covers(g)) return cross_tc_backward_splits(g);
     const int sms = sm_count();
     const long long ctas = (long long)((g.Lk + 63) / 64) * g.kv_heads * g.B;
     if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return 1;
@@ -457,9 +457,10 @@ int cross_backward_splits(const CrossGeom& g, bool bf16) {
 bra_status cross_backward_bf16(const CrossGeom& g, int splits, const void* q, const void* k, const void* v,
                                const void* o, const float* lse, const void* grad_o, void* dq, void* dk, void* dv,
                                float* delta, float* parts, int* status, cudaStream_t stream) {
-    (void)status;
     const bra_status rc =
-        g.d == 32   ? launch_d<32>(g, splits, q, k, v, o, lse, grad_o, dq, dk, dv, delta, parts, stream)
+        cross_tc_backward_covers(g)
+            ? cross_backward_tc(g, splits, q, k, v, o, lse, grad_o, dq, dk, dv, delta, parts, status, stream)
+        : g.d == 32 ? launch_d<32>(g, splits, q, k, v, o, lse, grad_o, dq, dk, dv, delta, parts, stream)
         : g.d == 64 ? launch_d<64>(g, splits, q, k, v, o, lse, grad_o, dq, dk, dv, delta, parts, stream)
                     : launch_d<128>(g, splits, q, k, v, o, lse, grad_o, dq, dk, dv, delta, parts, stream);
     if (rc != BRA_OK || splits == 1) return rc;

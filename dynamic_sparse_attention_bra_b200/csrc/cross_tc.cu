@@ -28,7 +28,7 @@
 // Bound by the exponentials (16 a clock and SM) for d = 32, by them and the
 // products for d = 128.  Every mbarrier wait is bounded; on expiry the kernel
 // records kDevTimeout, stops all roles, drains its products and frees TMEM.
-#include "cross_tile.cuh"
+#include "cross_tc.cuh"
 #include "kernels.h"
 #include "tma_host.h"
 
@@ -40,7 +40,6 @@ using namespace cross;
 constexpr int kCtrl = 3;
 constexpr int kThreads = 32 * (kCtrl + 8);
 constexpr int kStages = 4;  // at most
-constexpr uint32_t kWait = 1u << 22;
 constexpr float kGrow = 8.f;  // powers of two a maximum may grow by before O is rescaled
 
 struct Barriers {
@@ -69,43 +68,6 @@ struct Cfg {
     static constexpr uint32_t kOffBar = kOffKv + (uint32_t)kRing * 2u * kKvTile;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
 };
-
-// Byte offset of 16-byte chunk c of row r in a tile of ``rows`` rows: 64-byte
-// rows with the 64-byte swizzle at D = 32; 128-byte rows with the 128-byte
-// swizzle otherwise, channels 64.. of D = 128 in a second panel.
-template <int D>
-__device__ __forceinline__ uint32_t op_offset(int r, int c, int rows) {
-    if constexpr (D == 32) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-// Descriptor of a K-major operand (rows x D) at its k-th 16 channels.
-template <int D>
-__device__ __forceinline__ uint64_t k_major(uint32_t tile, int kk, int rows) {
-    if constexpr (D == 32) return ptx::smem_desc(tile + kk * 32, 16, 512, ptx::kSwizzle64B);
-    return ptx::smem_desc(tile + (uint32_t)((kk >> 2) * rows * 128 + (kk & 3) * 32), 16, 1024, ptx::kSwizzle128B);
-}
-// Descriptor of V (rows x D, channels the N axis) at its k-th 16 states.
-template <int D>
-__device__ __forceinline__ uint64_t v_operand(uint32_t tile, int kk, int rows) {
-    if constexpr (D == 32) return ptx::smem_desc(tile + kk * 1024, 16, 512, ptx::kSwizzle64B);
-    return ptx::smem_desc(tile + kk * 2048, rows * 128, 1024, ptx::kSwizzle128B);
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Barriers* sb, int* status) {
-    for (uint32_t i = 0; i < kWait; ++i) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((i & 1023) == 1023 && *reinterpret_cast<volatile int*>(&sb->abort) != 0) return false;
-    }
-    *reinterpret_cast<volatile int*>(&sb->abort) = 1;
-    raise_status(status, kDevTimeout);
-    return false;
-}
-
-// The same for a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Barriers* sb, int* status) {
-    if (__all_sync(0xffffffffu, ptx::mbar_test(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, sb, status));
-}
 
 struct TcPlan {
     int pairs;    // units of 256 rows in a (entry, state head)
@@ -192,10 +154,10 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // S = Q K^T of block ``at`` (the tile's b-th)
             auto qk = [&](const Unit& x, int b, int at) -> bool {
                 const int stage = at % kRing, buf = at % NB;
-                if (!wait_or_abort(&sb->kv_full[stage], (at / kRing) & 1, sb, status)) return false;
+                if (!wait_or_abort(&sb->kv_full[stage], (at / kRing) & 1, &sb->abort, status)) return false;
                 // the buffer's last S: read, or (P shares its columns) used by its P V
                 if (at >= NB && !wait_or_abort(C::kAlias ? &sb->o_done[grp][buf] : &sb->s_free[grp][buf],
-                                               (at / NB - 1) & 1, sb, status))
+                                               (at / NB - 1) & 1, &sb->abort, status))
                     return false;
                 ptx::tc_fence_after();
                 const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
@@ -211,7 +173,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // O += P V
             auto pv = [&](const Unit& x, int b, int at) -> bool {
                 const int stage = at % kRing, buf = at % NB;
-                if (!wait_or_abort(&sb->p_full[grp][buf], (at / NB) & 1, sb, status)) return false;
+                if (!wait_or_abort(&sb->p_full[grp][buf], (at / NB) & 1, &sb->abort, status)) return false;
                 ptx::tc_fence_after();
                 const uint32_t vt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile;
                 const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
@@ -225,7 +187,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
                 const Unit x = unit_at<BN>(g, p, u);
                 if (x.nb == 0) continue;
-                ok = wait_or_abort(&sb->q_full[grp][use & 1], (use >> 1) & 1, sb, status) && qk(x, 0, i);
+                ok = wait_or_abort(&sb->q_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status) && qk(x, 0, i);
                 for (int b = 0; ok && b < x.nb; ++b) ok = (b + 1 == x.nb || qk(x, b + 1, i + b + 1)) && pv(x, b, i + b);
                 i += x.nb;
                 ++use;
@@ -249,7 +211,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             if (x.nb == 0) continue;
             for (int grp = 0; grp < 2; ++grp) {
                 uint64_t* full = &sb->q_full[grp][use & 1];
-                if (use >= 2 && !warp_wait(&sb->q_empty[grp][use & 1], ((use >> 1) - 1) & 1, sb, status)) {
+                if (use >= 2 && !warp_wait(&sb->q_empty[grp][use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -290,7 +252,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                                          key < x.n && (!g.kv_mask || __ldcg(g.kv_mask + (size_t)x.b * g.Lk + key) != 0));
                     every &= w[h];
                 }
-                if (i >= kRing && !warp_wait(&sb->kv_empty[stage], ((i / kRing) - 1) & 1, sb, status)) {
+                if (i >= kRing && !warp_wait(&sb->kv_empty[stage], ((i / kRing) - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -350,7 +312,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             for (int b = 0; b < x.nb; ++b, ++i) {
                 const int buf = i % NB, phase = i / NB;
                 const uint32_t scol = cols + (uint32_t)buf * 64u;
-                if (!warp_wait(&sb->s_full[grp][buf], phase & 1, sb, status)) {
+                if (!warp_wait(&sb->s_full[grp][buf], phase & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -366,7 +328,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 const int left = x.n - (x.t0 + b) * BN;
                 if (g.kv_mask || left < BN) {
                     // (the block's loads are done; the wait makes the loader's words visible)
-                    if (g.kv_mask && !warp_wait(&sb->kv_full[i % kRing], (i / kRing) & 1, sb, status)) {
+                    if (g.kv_mask && !warp_wait(&sb->kv_full[i % kRing], (i / kRing) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
@@ -391,7 +353,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             ptx::max3(mx[(e >> 1) & 3], __uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1]));
                 const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
                 // P's buffer: its last P V is done
-                if (i >= NB && !warp_wait(&sb->o_done[grp][buf], (phase - 1) & 1, sb, status)) {
+                if (i >= NB && !warp_wait(&sb->o_done[grp][buf], (phase - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -399,7 +361,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     m = mn;
                 } else if (__any_sync(0xffffffffu, mn > m + kGrow)) {
                     // O stands still once the previous block's P V is done
-                    if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, sb, status)) {
+                    if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
@@ -454,7 +416,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, sb, status)) break;
+                if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) break;
                 ptx::tc_fence_after();
             }
             float lo, hi;

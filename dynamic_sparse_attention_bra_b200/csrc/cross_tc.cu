@@ -67,6 +67,7 @@ struct Cfg {
     static constexpr uint32_t kOffKv = 4 * kQTile;  // Q [group][2], then stages of K | V
     static constexpr uint32_t kOffBar = kOffKv + (uint32_t)kRing * 2u * kKvTile;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
+    static_assert(kSmem <= 227u * 1024u, "shared memory");
 };
 
 struct TcPlan {

@@ -12,11 +12,17 @@
 //   dK += dS Q,   dV += P dO                (rows of states)
 // whose sums stay in TMEM over all blocks.
 //
-// A unit is two tiles (one at d = 128: its sums take 256 of the 512 columns)
-// that share the streamed blocks; while one tile's products run, the other's
-// threads have the exponentials.  Roles of the warps: 0, 1 issue the products
-// of tile 0, 1; 2 loads (TMA; tiles and blocks with a masked or missing state by
-// cp.async, those rows filled with zeros); 3-6, 7-10 have a row a thread.
+// S and dP have two buffers (256 columns; the sums take 2 d of the others), so
+// that the products of the next block run under the exponentials of this one.
+// There is no maximum to agree on, so two threads share a row, 32 columns each.
+// Roles of the 12 warps: 0 issues S and dP, 1 the sums' products; 2 starts the
+// loads (TMA, or cp.async where no map can be made); 3 passes each landed tile
+// on, after it has zeroed the rows of masked or missing states (what is stored
+// there must not reach a product) and, for dK and dV, added the columns' log sums
+// and D; 4-7 and 8-11 are the rows' threads, left and right columns.
+// With two tiles of 128 rows a CTA, one buffer, and a thread a row (the first
+// form) a block's products and exponentials took turns: 4250 clocks for two
+// tiles, of which a row's threads waited 2360.
 // Every mbarrier wait is bounded; on expiry the kernel records kDevTimeout, stops
 // all roles, drains its products and frees TMEM.
 #include "cross_tc.cuh"
@@ -28,36 +34,38 @@ namespace {
 
 using namespace cross;
 
-constexpr int kCtrl = 3;
+constexpr int kCtrl = 4;
+constexpr int kThreads = 32 * (kCtrl + 8);
 constexpr int kStages = 4;  // at most
 constexpr int BN = 64;      // columns of a block
 
 struct Barriers {
-    uint64_t c_full[kStages], c_empty[kStages];
-    uint64_t r_full[2][2], r_empty[2][2];  // [tile][buffer]
-    uint64_t s_full[2], p_full[2], acc_done[2], drain[2];
-    uint32_t words[kStages][2];  // dQ: the block's valid states, where a mask says which
+    uint64_t c_land[kStages], c_full[kStages], c_empty[kStages];
+    uint64_t r_land[2], r_full[2], r_empty[2];
+    uint64_t s_full[2], p_full[2], acc_done[2];  // [buffer]
+    uint64_t rest_full, drain[2];
+    uint32_t words[kStages][2];  // dQ: the block's valid states
     uint32_t tmem;
     int abort;
 };
 
 template <int D>
 struct Cfg {
-    static constexpr int kTiles = D == 128 ? 1 : 2;
-    static constexpr int kThreads = 32 * (kCtrl + 4 * kTiles);
-    static constexpr uint32_t kTileCols = 256;  // TMEM columns from tile to tile
-    static constexpr uint32_t kDp = 64, kAcc1 = 128, kAcc2 = 128 + D;
+    // TMEM: buffer x: S at 128 x, dP at 128 x + 64 (P and dS over their first halves); sums
+    static constexpr uint32_t kDp = 64, kAcc1 = 256, kAcc2 = 256 + D;
     static constexpr uint32_t kRow = 128u * D * 2u, kCol = (uint32_t)BN * D * 2u;
     static constexpr int kRing = D == 128 ? 3 : 4;
-    // rows [tile][buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics, barriers
-    static constexpr uint32_t kOffCol = kTiles * 2 * 2 * kRow;
+    // rows [buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics (dQ: a row's sum of dS over its
+    // left, right columns), barriers
+    static constexpr uint32_t kOffCol = 2 * 2 * kRow;
     static constexpr uint32_t kOffStat = kOffCol + kRing * 2 * kCol;
     static constexpr uint32_t kOffBar = kOffStat + kRing * 2 * BN * 4;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
+    static_assert(kSmem <= 227u * 1024u && kRing * 2 * BN >= 2 * 128, "shared memory");
 };
 
 struct BwdPlan {
-    int groups;         // units of kTiles x 128 rows in a (entry, state head)
+    int tiles;          // of 128 rows in a (entry, state head)
     int splits;         // dK, dV: parts of the rows of queries
     int units;
     int tma_r, tma_c;   // loads by TMA (the maps could be made)
@@ -67,11 +75,11 @@ struct Unit {
     int b, j, row0, split, n, t0, nb;  // first block and number of blocks
 };
 
-template <bool STATES, int TILE_ROWS>
+template <bool STATES>
 __device__ __forceinline__ Unit unit_at(const CrossGeom& g, const BwdPlan& p, int u) {
     Unit x;
-    x.row0 = (u % p.groups) * TILE_ROWS;
-    u /= p.groups;
+    x.row0 = (u % p.tiles) * 128;
+    u /= p.tiles;
     x.split = u % p.splits;
     u /= p.splits;
     x.j = u % g.kv_heads;
@@ -107,20 +115,29 @@ __device__ __forceinline__ void load_queries(uint32_t dst, const __nv_bfloat16* 
     }
 }
 
-// ``rows`` rows of states from key0; rows whose bit in w is off: zeros.
-template <int D, int W>
-__device__ __forceinline__ void load_states(uint32_t dst, const __nv_bfloat16* base, long long step, int key0,
-                                            const uint32_t (&w)[W], int rows, int tile_rows, int lane) {
+// ``rows`` rows of states from key0, those from ``end`` on not read.
+template <int D>
+__device__ __forceinline__ void load_states(uint32_t dst, const __nv_bfloat16* base, long long step, int key0, int end,
+                                            int rows, int lane) {
 #pragma unroll 4
     for (int e = lane; e < rows * (D / 8); e += 32) {
         const int r = e / (D / 8), c = e % (D / 8);
-        uint32_t word = w[0];
-#pragma unroll
-        for (int h = 1; h < W; ++h) word = r >= h * 32 ? w[h] : word;
-        const bool on = (word >> (r & 31)) & 1u;
-        ptx::cp_async16_zfill(dst + op_offset<D>(r, c, tile_rows), on ? base + (size_t)(key0 + r) * step + c * 8 : base,
+        const bool on = key0 + r < end;
+        ptx::cp_async16_zfill(dst + op_offset<D>(r, c, rows), on ? base + (size_t)(key0 + r) * step + c * 8 : base,
                               on ? 16u : 0u);
     }
+}
+
+// Zeros in the rows of two tiles (``second`` bytes apart) whose bit in w is off.
+template <int D, int W>
+__device__ __forceinline__ void clear_states(uint32_t dst, uint32_t second, const uint32_t (&w)[W], int lane) {
+    for (int h = 0; h < W; ++h)
+        for (uint32_t off = ~w[h]; off != 0u; off &= off - 1u) {
+            const int r = h * 32 + __ffs(off) - 1;
+            for (int c = lane; c < D / 4; c += 32)
+                ptx::st_shared_v4(dst + (c >= D / 8 ? second : 0u) + op_offset<D>(r, c & (D / 8 - 1), W * 32), 0u, 0u, 0u,
+                                  0u);
+        }
 }
 
 // Validity of 32 W states from key0 as bits; true if all are.
@@ -139,14 +156,14 @@ __device__ __forceinline__ bool valid_words(const CrossGeom& g, int b, int n, in
 // STATES: the rows are states (dK, dV), the columns queries; else the rows are
 // queries (dQ), the columns states.
 template <int D, bool STATES>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __grid_constant__ CUtensorMap tr2,
                              const __grid_constant__ CUtensorMap tc1, const __grid_constant__ CUtensorMap tc2,
                              const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                              const __nv_bfloat16* o, const float* lse, const __nv_bfloat16* go, __nv_bfloat16* out1,
                              __nv_bfloat16* out2, float* delta, float* parts, CrossGeom g, BwdPlan p, int* status) {
     using C = Cfg<D>;
-    constexpr int kRing = C::kRing, kTileRows = 128 * C::kTiles;
+    constexpr int kRing = C::kRing;
     constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -156,19 +173,20 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(&sb->c_land[i], 1);
             ptx::mbar_init(&sb->c_full[i], 1);
-            ptx::mbar_init(&sb->c_empty[i], C::kTiles);
+            ptx::mbar_init(&sb->c_empty[i], 1);
         }
         for (int x = 0; x < 2; ++x) {
-            for (int y = 0; y < 2; ++y) {
-                ptx::mbar_init(&sb->r_full[x][y], 1);
-                ptx::mbar_init(&sb->r_empty[x][y], STATES ? 1 : 1 + 128);  // the products; the reads of dO for D
-            }
+            ptx::mbar_init(&sb->r_land[x], 1);
+            ptx::mbar_init(&sb->r_full[x], 1);
+            ptx::mbar_init(&sb->r_empty[x], STATES ? 1 : 1 + 256);  // the products; the reads of dO for D
             ptx::mbar_init(&sb->s_full[x], 1);
-            ptx::mbar_init(&sb->p_full[x], 128);
+            ptx::mbar_init(&sb->p_full[x], 256);
             ptx::mbar_init(&sb->acc_done[x], 1);
             ptx::mbar_init(&sb->drain[x], 1);
         }
+        ptx::mbar_init(&sb->rest_full, 256);
         sb->abort = 0;
         ptx::mbar_init_fence();
     }
@@ -182,61 +200,77 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
     const uint32_t tmem = sb->tmem;
     grid_dependency_wait();
 
-    if (warp < 2) {
-        // ------------------------------------------------ products of tile ``warp``
-        if (lane == 0 && warp < C::kTiles) {
-            const int grp = warp;
-            const uint32_t cols = tmem + (uint32_t)grp * C::kTileCols;
-            const uint32_t idesc_acc = ptx::idesc_bf16_f32(128, D, false, true);
+    auto col_tile = [&](int stage) { return sbase + C::kOffCol + (uint32_t)stage * 2u * C::kCol; };
+    auto row_tile = [&](int use) { return sbase + (uint32_t)(use & 1) * 2u * C::kRow; };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- S and dP
+        if (lane == 0) {
             int i = 0, use = 0;  // blocks and units so far
             bool ok = true;
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const Unit x = unit_at<STATES, kTileRows>(g, p, u);
+                const Unit x = unit_at<STATES>(g, p, u);
                 if (x.nb == 0) continue;
-                ok = wait_or_abort(&sb->r_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status);
-                const uint32_t r1 = sbase + (uint32_t)(grp * 2 + (use & 1)) * 2u * C::kRow;
+                ok = wait_or_abort(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status);
+                const uint32_t r1 = row_tile(use);
                 for (int b = 0; ok && b < x.nb; ++b, ++i) {
-                    const int stage = i % kRing;
-                    const uint32_t c1 = sbase + C::kOffCol + (uint32_t)stage * 2u * C::kCol;
-                    // the columns of S and dP hold the last block's P and dS until their products end
+                    const int stage = i % kRing, buf = i & 1;
+                    const uint32_t c1 = col_tile(stage), cols = tmem + (uint32_t)buf * 128u;
+                    // the buffer holds the P and dS of two blocks ago until their products end
                     if (!wait_or_abort(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status) ||
-                        (i > 0 && !wait_or_abort(&sb->acc_done[grp], (i - 1) & 1, &sb->abort, status))) {
+                        (i >= 2 && !wait_or_abort(&sb->acc_done[buf], ((i >> 1) - 1) & 1, &sb->abort, status))) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const int nc = block_cols<STATES>(x, b);
-                    const uint32_t idesc = ptx::idesc_bf16_f32(128, nc, false, false);
+                    const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<STATES>(x, b), false, false);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         ptx::mma_bf16(cols, k_major<D>(r1, kk, 128), k_major<D>(c1, kk, BN), idesc, kk);
                         ptx::mma_bf16(cols + C::kDp, k_major<D>(r1 + C::kRow, kk, 128), k_major<D>(c1 + C::kCol, kk, BN),
                                       idesc, kk);
                     }
-                    ptx::mma_commit(&sb->s_full[grp]);
-                    if (b == x.nb - 1) ptx::mma_commit(&sb->r_empty[grp][use & 1]);
-                    if (!wait_or_abort(&sb->p_full[grp], i & 1, &sb->abort, status)) {
+                    ptx::mma_commit(&sb->s_full[buf]);
+                    if (b == x.nb - 1) ptx::mma_commit(&sb->r_empty[use & 1]);
+                }
+                ++use;
+            }
+            ptx::mma_commit(&sb->drain[0]);
+            ptx::mbar_wait(&sb->drain[0], 0, kWait);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- the sums
+        if (lane == 0) {
+            const uint32_t idesc = ptx::idesc_bf16_f32(128, D, false, true);
+            int i = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
+                const Unit x = unit_at<STATES>(g, p, u);
+                for (int b = 0; b < x.nb; ++b, ++i) {
+                    const int stage = i % kRing, buf = i & 1;
+                    const uint32_t c1 = col_tile(stage), c2 = STATES ? c1 + C::kCol : c1;
+                    const uint32_t cols = tmem + (uint32_t)buf * 128u;
+                    if (!wait_or_abort(&sb->p_full[buf], (i >> 1) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t c_acc2 = STATES ? c1 + C::kCol : c1;
-                    for (int kk = 0; kk < (nc >> 4); ++kk) {
-                        ptx::mma_bf16_ta(cols + C::kAcc1, cols + C::kDp + (uint32_t)kk * 8u, v_operand<D>(c1, kk, BN),
-                                         idesc_acc, b > 0 || kk > 0);
-                        ptx::mma_bf16_ta(cols + C::kAcc2, cols + (uint32_t)kk * 8u, v_operand<D>(c_acc2, kk, BN),
-                                         idesc_acc, b > 0 || kk > 0);
+                    const int steps = block_cols<STATES>(x, b) >> 4;
+                    for (int kk = 0; kk < steps; ++kk) {  // 16 columns: of the left half for kk < 2
+                        const uint32_t a = cols + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8);
+                        ptx::mma_bf16_ta(tmem + C::kAcc1, a + C::kDp, v_operand<D>(c1, kk, BN), idesc, b > 0 || kk > 0);
+                        ptx::mma_bf16_ta(tmem + C::kAcc2, a, v_operand<D>(c2, kk, BN), idesc, b > 0 || kk > 0);
                     }
-                    ptx::mma_commit(&sb->acc_done[grp]);
+                    ptx::mma_commit(&sb->acc_done[buf]);
                     ptx::mma_commit(&sb->c_empty[stage]);
                 }
-                ++use;
             }
-            ptx::mma_commit(&sb->drain[grp]);
-            ptx::mbar_wait(&sb->drain[grp], 0, kWait);
+            ptx::mma_commit(&sb->drain[1]);
+            ptx::mbar_wait(&sb->drain[1], 0, kWait);
         }
         __syncwarp();
-    } else if (warp < kCtrl) {
+    } else if (warp == 2) {
         // ------------------------------------------------------------------ loads
         if (lane == 0) {
             ptx::tma_prefetch_desc(&tr1);
@@ -247,87 +281,90 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         int i = 0, use = 0;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at<STATES, kTileRows>(g, p, u);
+            const Unit x = unit_at<STATES>(g, p, u);
             if (x.nb == 0) continue;
-            const __nv_bfloat16* kbase = k + (size_t)x.b * g.k_batch + (size_t)x.j * D;
-            const __nv_bfloat16* vbase = v + (size_t)x.b * g.v_batch + (size_t)x.j * D;
-            // TMA of one box of states (rows from key0) or queries (rows from r0), R or C operands
-            auto tma_states = [&](uint32_t dst, uint32_t second, const CUtensorMap* m1, const CUtensorMap* m2, int key0,
-                                  uint32_t rows, uint64_t* full) {
-                ptx::mbar_arrive_expect_tx(full, 2u * rows * D * 2u);
+            // ``rows`` rows from r0 of both operands, states or queries, to dst and dst + second
+            auto load = [&](uint32_t dst, uint32_t second, bool states, int r0, int rows, int tma, const CUtensorMap* m1,
+                            const CUtensorMap* m2, uint64_t* land) {
+                if (tma) {
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(land, 2u * (uint32_t)rows * D * 2u);
+                        const int head = states ? x.j : x.j * g.rep, at = states ? r0 : r0 / g.rep;
+                        const int b1 = (states ? g.k_batch : g.q_batch) ? x.b : 0, b2 = states && !g.v_batch ? 0 : x.b;
 #pragma unroll
-                for (int c = 0; c < kPanels; ++c) {
-                    ptx::tma_load_4d(dst + (uint32_t)c * rows * 128u, m1, c * 64, x.j, key0, g.k_batch ? x.b : 0, full);
-                    ptx::tma_load_4d(dst + second + (uint32_t)c * rows * 128u, m2, c * 64, x.j, key0,
-                                     g.v_batch ? x.b : 0, full);
-                }
-            };
-            auto tma_queries = [&](uint32_t dst, uint32_t second, const CUtensorMap* m1, const CUtensorMap* m2, int r0,
-                                   uint32_t rows, uint64_t* full) {
-                ptx::mbar_arrive_expect_tx(full, 2u * rows * D * 2u);
-#pragma unroll
-                for (int c = 0; c < kPanels; ++c) {
-                    ptx::tma_load_4d(dst + (uint32_t)c * rows * 128u, m1, c * 64, x.j * g.rep, r0 / g.rep,
-                                     g.q_batch ? x.b : 0, full);
-                    ptx::tma_load_4d(dst + second + (uint32_t)c * rows * 128u, m2, c * 64, x.j * g.rep, r0 / g.rep, x.b,
-                                     full);
-                }
-            };
-            auto landed = [&](uint64_t* full) {  // this warp's cp.async and stores, seen by the products
-                ptx::cp_async_wait_all();
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full);
-            };
-            for (int grp = 0; grp < C::kTiles; ++grp) {
-                uint64_t* full = &sb->r_full[grp][use & 1];
-                if (use >= 2 && !warp_wait(&sb->r_empty[grp][use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t r1 = sbase + (uint32_t)(grp * 2 + (use & 1)) * 2u * C::kRow;
-                const int row0 = x.row0 + grp * 128;
-                if constexpr (STATES) {
-                    uint32_t w[4];
-                    if (valid_words(g, x.b, x.n, row0, lane, w) && p.tma_r) {
-                        if (lane == 0) tma_states(r1, C::kRow, &tr1, &tr2, row0, 128, full);
-                    } else {
-                        load_states<D>(r1, kbase, g.k_row, row0, w, 128, 128, lane);
-                        load_states<D>(r1 + C::kRow, vbase, g.v_row, row0, w, 128, 128, lane);
-                        landed(full);
+                        for (int c = 0; c < kPanels; ++c) {
+                            ptx::tma_load_4d(dst + (uint32_t)(c * rows) * 128u, m1, c * 64, head, at, b1, land);
+                            ptx::tma_load_4d(dst + second + (uint32_t)(c * rows) * 128u, m2, c * 64, head, at, b2, land);
+                        }
                     }
                 } else {
-                    if (p.tma_r) {
-                        if (lane == 0) tma_queries(r1, C::kRow, &tr1, &tr2, row0, 128, full);
+                    if (states) {
+                        load_states<D>(dst, k + (size_t)x.b * g.k_batch + (size_t)x.j * D, g.k_row, r0, x.n, rows, lane);
+                        load_states<D>(dst + second, v + (size_t)x.b * g.v_batch + (size_t)x.j * D, g.v_row, r0, x.n,
+                                       rows, lane);
                     } else {
-                        load_queries<D>(r1, q, false, g, x.b, x.j, row0, 128, lane);
-                        load_queries<D>(r1 + C::kRow, go, true, g, x.b, x.j, row0, 128, lane);
-                        landed(full);
+                        load_queries<D>(dst, q, false, g, x.b, x.j, r0, rows, lane);
+                        load_queries<D>(dst + second, go, true, g, x.b, x.j, r0, rows, lane);
                     }
-                }
-            }
-            float st[4];  // STATES: this lane's share of the next block's log sums (2) and D (2)
-            auto read_stats = [&](int b) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = (x.t0 + b) * BN + h * 32 + lane;
-                    const bool in = b < x.nb && r < g.rows;
-                    const size_t at = in ? cross_lse_offset(g, x.b, x.j, r) : 0;
-                    st[h] = in ? __ldcg(lse + at) : -INFINITY;
-                    st[2 + h] = in ? __ldcg(delta + at) : 0.f;
+                    ptx::cp_async_wait_all();
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(land);
                 }
             };
-            if (STATES) read_stats(0);
-            for (int b = 0; ok && b < x.nb; ++b, ++i) {
-                const int stage = i % kRing, t = x.t0 + b;
-                uint32_t w[2];
-                const bool whole = STATES || valid_words(g, x.b, x.n, t * BN, lane, w);
+            if (use >= 2 && !warp_wait(&sb->r_empty[use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) break;
+            load(row_tile(use), C::kRow, STATES, x.row0, 128, p.tma_r, &tr1, &tr2, &sb->r_land[use & 1]);
+            for (int b = 0; b < x.nb; ++b, ++i) {
+                const int stage = i % kRing;
                 if (i >= kRing && !warp_wait(&sb->c_empty[stage], ((i / kRing) - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
-                const uint32_t c1 = sbase + C::kOffCol + (uint32_t)stage * 2u * C::kCol;
-                uint64_t* full = &sb->c_full[stage];
+                load(col_tile(stage), C::kCol, !STATES, (x.t0 + b) * BN, BN, p.tma_c, &tc1, &tc2, &sb->c_land[stage]);
+            }
+            ++use;
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------- landed tiles, passed to the products
+        int i = 0, use = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
+            const Unit x = unit_at<STATES>(g, p, u);
+            if (x.nb == 0) continue;
+            auto pass = [&](uint64_t* full) {  // this warp's stores, seen by the products and the rows' threads
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(full);
+            };
+            uint32_t wr[4];
+            bool whole = true;
+            if (STATES) whole = valid_words(g, x.b, x.n, x.row0, lane, wr);
+            if (!warp_wait(&sb->r_land[use & 1], (use >> 1) & 1, &sb->abort, status)) break;
+            if (STATES && !whole) clear_states<D>(row_tile(use), C::kRow, wr, lane);
+            pass(&sb->r_full[use & 1]);
+            float st[4];  // STATES: this lane's share of a block's log sums (2) and D (2), read a block ahead
+            uint32_t w[2];
+            auto ahead = [&](int b) {
+                if constexpr (STATES) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = (x.t0 + b) * BN + h * 32 + lane;
+                        const bool in = b < x.nb && r < g.rows;
+                        const size_t at = in ? cross_lse_offset(g, x.b, x.j, r) : 0;
+                        st[h] = in ? __ldcg(lse + at) : -INFINITY;
+                        st[2 + h] = in ? __ldcg(delta + at) : 0.f;
+                    }
+                } else {
+                    whole = b >= x.nb || valid_words(g, x.b, x.n, (x.t0 + b) * BN, lane, w);
+                }
+            };
+            ahead(0);
+            for (int b = 0; b < x.nb; ++b, ++i) {
+                const int stage = i % kRing;
+                if (!warp_wait(&sb->c_land[stage], (i / kRing) & 1, &sb->abort, status)) {
+                    ok = false;
+                    break;
+                }
                 if constexpr (STATES) {
                     float* stat = reinterpret_cast<float*>(smem + C::kOffStat) + stage * 2 * BN;
 #pragma unroll
@@ -335,46 +372,30 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                         stat[h * 32 + lane] = -exponent_offset(st[h]);
                         stat[BN + h * 32 + lane] = -st[2 + h];
                     }
-                    __syncwarp();
-                    if (p.tma_c) {
-                        if (lane == 0) tma_queries(c1, C::kCol, &tc1, &tc2, t * BN, BN, full);
-                    } else {
-                        load_queries<D>(c1, q, false, g, x.b, x.j, t * BN, BN, lane);
-                        load_queries<D>(c1 + C::kCol, go, true, g, x.b, x.j, t * BN, BN, lane);
-                        landed(full);
-                    }
-                    read_stats(b + 1);
                 } else {
-                    if (lane == 0 && g.kv_mask) {
-                        sb->words[stage][0] = w[0];
-                        sb->words[stage][1] = w[1];
-                    }
-                    if (whole && p.tma_c) {
-                        if (lane == 0) tma_states(c1, C::kCol, &tc1, &tc2, t * BN, BN, full);
-                    } else {
-                        const int rows = block_cols<false>(x, b);  // no product reads past them
-                        load_states<D>(c1, kbase, g.k_row, t * BN, w, rows, BN, lane);
-                        load_states<D>(c1 + C::kCol, vbase, g.v_row, t * BN, w, rows, BN, lane);
-                        landed(full);
-                    }
+                    if (lane < 2) sb->words[stage][lane] = w[lane];
+                    if (!whole) clear_states<D>(col_tile(stage), C::kCol, w, lane);
                 }
+                pass(&sb->c_full[stage]);
+                ahead(b + 1);
             }
             ++use;
         }
     } else {
         // ---------------------------------------------------- P, dS and the epilogue
-        const int grp = (warp - kCtrl) >> 2, qd = warp & 3;
+        const int half = (warp - kCtrl) >> 2, qd = warp & 3;
         const int row = 32 * qd + lane;
-        const uint32_t cols = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)grp * C::kTileCols;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16);
         const float c2 = g.scale * kLog2e;
+        const uint64_t c22 = ptx::pack_f32x2(c2, c2);
         int i = 0, use = 0;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at<STATES, kTileRows>(g, p, u);
-            const int r0 = x.row0 + grp * 128 + row;
+            const Unit x = unit_at<STATES>(g, p, u);
+            const int r0 = x.row0 + row;
             const bool in = r0 < (STATES ? g.Lk : g.rows);
-            float noff = -INFINITY, nd = 0.f, rest = 0.f;  // dQ: the row's -offset and -D0; sum of dS
-            if (!STATES) {
+            float noff = -INFINITY, nd = 0.f;  // dQ: the row's -offset and -D0
+            if (!STATES && x.nb > 0) {
                 // D0 = <dO, O>: O from memory, dO from the tile
                 float d0 = 0.f;
                 const size_t off = in ? cross_o_offset(g, x.b, x.j, r0) : 0;
@@ -383,111 +404,117 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 for (int c = 0; c < D / 8; ++c)
                     ov[c] = in ? __ldcg(reinterpret_cast<const uint4*>(o + off) + c) : make_uint4(0u, 0u, 0u, 0u);
                 if (in) noff = -exponent_offset(__ldcg(lse + cross_lse_offset(g, x.b, x.j, r0)));
-                if (x.nb > 0) {
-                    if (!warp_wait(&sb->r_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status)) break;
-                    const uint8_t* r2 = smem + (size_t)(grp * 2 + (use & 1)) * 2 * C::kRow + C::kRow;
+                if (!warp_wait(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status)) break;
+                const uint8_t* r2 = smem + (size_t)(use & 1) * 2 * C::kRow + C::kRow;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        float a[8], h[8];
-                        unpack16(ov[c], a, (const __nv_bfloat16*)nullptr);
-                        unpack16(*reinterpret_cast<const uint4*>(r2 + op_offset<D>(row, c, 128)), h,
-                                 (const __nv_bfloat16*)nullptr);
+                for (int c = 0; c < D / 8; ++c) {
+                    float a[8], h[8];
+                    unpack16(ov[c], a, (const __nv_bfloat16*)nullptr);
+                    unpack16(*reinterpret_cast<const uint4*>(r2 + op_offset<D>(row, c, 128)), h,
+                             (const __nv_bfloat16*)nullptr);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d0 = fmaf(a[e], h[e], d0);
-                    }
-                    ptx::mbar_arrive(&sb->r_empty[grp][use & 1]);
+                    for (int e = 0; e < 8; ++e) d0 = fmaf(a[e], h[e], d0);
                 }
+                ptx::mbar_arrive(&sb->r_empty[use & 1]);
                 nd = -d0;
             }
-            const uint64_t c22 = ptx::pack_f32x2(c2, c2);
             uint64_t rest2 = 0ull;
             for (int b = 0; b < x.nb; ++b, ++i) {
-                const int stage = i % kRing;
-                if (!warp_wait(&sb->s_full[grp], i & 1, &sb->abort, status) ||
-                    ((STATES || g.kv_mask) && !warp_wait(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status))) {
+                const int stage = i % kRing, buf = i & 1;
+                const uint32_t cols = lanes + (uint32_t)buf * 128u;
+                if (!warp_wait(&sb->s_full[buf], (i >> 1) & 1, &sb->abort, status) ||
+                    !warp_wait(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const int nc = block_cols<STATES>(x, b), left = x.n - (x.t0 + b) * BN;
-                const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!STATES && nc <= h * 32) break;
+                const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN + half * 32;
+                if (STATES || block_cols<STATES>(x, b) > half * 32) {
                     uint32_t s[32], dp[32];
-                    ptx::tmem_load_pair(cols + h * 32, cols + C::kDp + h * 32, s, dp);
-                    uint32_t w = 0xffffffffu;
-                    if (!STATES) {
-                        const int some = left - h * 32;
-                        w = g.kv_mask ? sb->words[stage][h] : (some >= 32 ? 0xffffffffu : (1u << max(some, 0)) - 1u);
-                    }
+                    ptx::tmem_load_pair(cols + half * 32, cols + C::kDp + half * 32, s, dp);
+                    const uint32_t w = STATES ? 0xffffffffu : sb->words[stage][half];
                     uint32_t pp[16], pd[16];
-                    const uint64_t noff2 = ptx::pack_f32x2(noff, noff), nd2 = ptx::pack_f32x2(nd, nd);
+                    auto form = [&](bool masked) {
+                        const uint64_t noff2 = ptx::pack_f32x2(noff, noff), nd2 = ptx::pack_f32x2(nd, nd);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        uint64_t no = noff2, dd = nd2;
-                        if constexpr (STATES) {
-                            no = *reinterpret_cast<const uint64_t*>(stat + h * 32 + 2 * e);
-                            dd = *reinterpret_cast<const uint64_t*>(stat + BN + h * 32 + 2 * e);
+                        for (int e = 0; e < 16; ++e) {
+                            uint64_t no = noff2, dd = nd2;
+                            if constexpr (STATES) {
+                                no = *reinterpret_cast<const uint64_t*>(stat + 2 * e);
+                                dd = *reinterpret_cast<const uint64_t*>(stat + BN + 2 * e);
+                            }
+                            float lo, hi, dlo, dhi;
+                            ptx::unpack_f32x2(
+                                ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                               c22, no),
+                                lo, hi);
+                            lo = ptx::ex2(lo);
+                            hi = ptx::ex2(hi);
+                            uint64_t ds = ptx::mul_f32x2(
+                                ptx::pack_f32x2(lo, hi),
+                                ptx::add_f32x2(
+                                    ptx::pack_f32x2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), dd));
+                            ptx::unpack_f32x2(ds, dlo, dhi);
+                            if (masked) {  // nothing, whatever the columns hold
+                                if (!((w >> (2 * e)) & 1u)) lo = dlo = 0.f;
+                                if (!((w >> (2 * e + 1)) & 1u)) hi = dhi = 0.f;
+                                ds = ptx::pack_f32x2(dlo, dhi);
+                            }
+                            if (!STATES) rest2 = ptx::add_f32x2(rest2, ds);
+                            pp[e] = ptx::pack_bf16x2(lo, hi);
+                            pd[e] = ptx::pack_bf16x2(dlo, dhi);
                         }
-                        float lo, hi;
-                        ptx::unpack_f32x2(
-                            ptx::fma_f32x2(ptx::pack_f32x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c22,
-                                           no),
-                            lo, hi);
-                        lo = ptx::ex2(lo);
-                        hi = ptx::ex2(hi);
-                        uint64_t ds = ptx::mul_f32x2(
-                            ptx::pack_f32x2(lo, hi),
-                            ptx::add_f32x2(ptx::pack_f32x2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])),
-                                           dd));
-                        float dlo, dhi;
-                        ptx::unpack_f32x2(ds, dlo, dhi);
-                        if (!STATES && w != 0xffffffffu) {  // (uniform) masked states: nothing, whatever the sums hold
-                            if (!((w >> (2 * e)) & 1u)) lo = dlo = 0.f;
-                            if (!((w >> (2 * e + 1)) & 1u)) hi = dhi = 0.f;
-                            ds = ptx::pack_f32x2(dlo, dhi);
-                        }
-                        if (!STATES) rest2 = ptx::add_f32x2(rest2, ds);
-                        pp[e] = ptx::pack_bf16x2(lo, hi);
-                        pd[e] = ptx::pack_bf16x2(dlo, dhi);
-                    }
-                    ptx::tmem_st16(cols + h * 16, pp);
-                    ptx::tmem_st16(cols + C::kDp + h * 16, pd);
+                    };
+                    if (STATES || w == 0xffffffffu) form(false);
+                    else form(true);
+                    // each side's over the first 16 of the scores that it has read itself
+                    ptx::tmem_st16(cols + half * 32, pp);
+                    ptx::tmem_st16(cols + C::kDp + half * 32, pd);
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&sb->p_full[grp]);
+                ptx::mbar_arrive(&sb->p_full[buf]);
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->acc_done[grp], (i - 1) & 1, &sb->abort, status)) break;
+                if (!warp_wait(&sb->acc_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &sb->abort, status)) break;
                 ptx::tc_fence_after();
-                ++use;
             }
             bool live = x.nb > 0;
+            float rest = 0.f;  // dQ: D - D0
             size_t at = 0;
             if (STATES) {
                 live = live && in && r0 < x.n && (!g.kv_mask || __ldcg(g.kv_mask + (size_t)x.b * g.Lk + r0) != 0);
                 if (in) at = (((size_t)x.b * g.Lk + r0) * g.kv_heads + x.j) * D;
             } else {
-                float lo, hi;
-                ptx::unpack_f32x2(rest2, lo, hi);
-                rest = lo + hi;
+                if (x.nb > 0) {
+                    float lo, hi;
+                    ptx::unpack_f32x2(rest2, lo, hi);
+                    float* rests = reinterpret_cast<float*>(smem + C::kOffStat);
+                    rests[half * 128 + row] = lo + hi;
+                    ptx::mbar_arrive(&sb->rest_full);
+                    if (!warp_wait(&sb->rest_full, use & 1, &sb->abort, status)) break;
+                    rest = rests[row] + rests[128 + row];
+                }
                 if (in) {
                     at = cross_o_offset(g, x.b, x.j, r0);
-                    delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
+                    if (half == 0) delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
                 }
             }
             const size_t elems = (size_t)g.B * g.Lk * g.kv_heads * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t a1[32], a2[32];
-                if (x.nb > 0) ptx::tmem_load_pair(cols + C::kAcc1 + c, cols + C::kAcc2 + c, a1, a2);
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                uint32_t a1[16], a2[16];
+                if (x.nb > 0) {
+                    ptx::tmem_ld16(lanes + C::kAcc1 + c, a1);
+                    ptx::tmem_ld16(lanes + C::kAcc2 + c, a2);
+                    ptx::tmem_wait16(a1);
+                    ptx::tmem_wait16(a2);
+                }
                 if (!in) continue;
-                float f1[32], f2[32];
+                float f1[16], f2[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     f1[e] = live ? __uint_as_float(a1[e]) : 0.f;
                     f2[e] = live ? __uint_as_float(a2[e]) : 0.f;
                     if (!STATES) f1[e] = fmaf(-rest, f2[e], f1[e]);
@@ -496,13 +523,13 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 if (STATES && p.splits > 1) {
                     float* out = parts + (size_t)x.split * 2 * elems + at + c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < 16; e += 4) {
                         *reinterpret_cast<float4*>(out + e) = make_float4(f1[e], f1[e + 1], f1[e + 2], f1[e + 3]);
                         *reinterpret_cast<float4*>(out + elems + e) = make_float4(f2[e], f2[e + 1], f2[e + 2], f2[e + 3]);
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
+                    for (int e = 0; e < 16; e += 8) {
                         *reinterpret_cast<uint4*>(out1 + at + c + e) =
                             make_uint4(ptx::pack_bf16x2(f1[e], f1[e + 1]), ptx::pack_bf16x2(f1[e + 2], f1[e + 3]),
                                        ptx::pack_bf16x2(f1[e + 4], f1[e + 5]), ptx::pack_bf16x2(f1[e + 6], f1[e + 7]));
@@ -513,6 +540,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     }
                 }
             }
+            if (x.nb > 0) ++use;
             ptx::tc_fence_before();  // the sums are read before the next tile's first products, which p_full orders after
         }
     }
@@ -545,10 +573,9 @@ bra_status launch(const CrossGeom& g, int splits, const void* q, const void* k, 
     using C = Cfg<D>;
     using T = __nv_bfloat16;
     BwdPlan p = {};
-    const int tile_rows = 128 * C::kTiles, length = STATES ? g.Lk : g.rows;
-    p.groups = (length + tile_rows - 1) / tile_rows;
+    p.tiles = ((STATES ? g.Lk : g.rows) + 127) / 128;
     p.splits = STATES ? splits : 1;
-    const long long units = (long long)p.groups * p.splits * g.kv_heads * g.B;
+    const long long units = (long long)p.tiles * p.splits * g.kv_heads * g.B;
     if (units == 0) return BRA_OK;
     if (units > 0x3fffffffLL) return BRA_ERR_UNSUPPORTED;
     p.units = (int)units;
@@ -566,7 +593,7 @@ bra_status launch(const CrossGeom& g, int splits, const void* q, const void* k, 
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
         return BRA_ERR_CUDA;
     const int grid = units < sms ? (int)units : sms;
-    const cudaError_t e = launch_after_previous(kernel, dim3(grid), dim3(C::kThreads), C::kSmem, stream, tr1, tr2, tc1,
+    const cudaError_t e = launch_after_previous(kernel, dim3(grid), dim3(kThreads), C::kSmem, stream, tr1, tr2, tc1,
                                                 tc2, (const T*)q, (const T*)k, (const T*)v, (const T*)o, lse,
                                                 (const T*)go, (T*)out1, (T*)out2, delta, parts, g, p, status);
     return e == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
@@ -588,8 +615,8 @@ bool cross_tc_backward_covers(const CrossGeom& g) { return g.rows >= 128 && g.Lk
 
 // Enough row splits for the tiles of states to reach every SM, each of at least eight blocks of rows.
 int cross_tc_backward_splits(const CrossGeom& g) {
-    const int sms = sm_count(), tile_rows = g.d == 128 ? 128 : 256;
-    const long long units = (long long)((g.Lk + tile_rows - 1) / tile_rows) * g.kv_heads * g.B;
+    const int sms = sm_count();
+    const long long units = (long long)((g.Lk + 127) / 128) * g.kv_heads * g.B;
     if (sms <= 0 || units <= 0 || units >= sms) return 1;
     long long s = sms / units;
     const long long most = ((g.rows + BN - 1) / BN) / 8;

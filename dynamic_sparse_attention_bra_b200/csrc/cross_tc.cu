@@ -161,12 +161,12 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                                                (at / NB - 1) & 1, &sb->abort, status))
                     return false;
                 ptx::tc_fence_after();
-                const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
-                const uint32_t kt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile;
+                const uint64_t qd = k_major<D>(sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile);
+                const uint64_t kd = k_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<BN>(x.n, x.t0 + b), false, false);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_bf16(cols + (uint32_t)buf * 64u, k_major<D>(qt, kk, 128), k_major<D>(kt, kk, BN), idesc, kk);
+                    ptx::mma_bf16(cols + (uint32_t)buf * 64u, qd + k_step<D>(kk, 128), kd + k_step<D>(kk, BN), idesc, kk);
                 ptx::mma_commit(&sb->s_full[grp][buf]);
                 if (b == x.nb - 1) ptx::mma_commit(&sb->q_empty[grp][use & 1]);
                 return true;
@@ -176,11 +176,14 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 const int stage = at % kRing, buf = at % NB;
                 if (!wait_or_abort(&sb->p_full[grp][buf], (at / NB) & 1, &sb->abort, status)) return false;
                 ptx::tc_fence_after();
-                const uint32_t vt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile;
+                const uint64_t vd = n_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile, BN);
                 const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
-                for (int kk = 0; kk < steps; ++kk)
-                    ptx::mma_bf16_ta(cols + C::kO, cols + C::kP + (uint32_t)buf * 64u + (uint32_t)kk * 8u,
-                                     v_operand<D>(vt, kk, BN), idesc_o, b > 0 || kk > 0);
+                const uint32_t pt = cols + C::kP + (uint32_t)buf * 64u;
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    if (kk < steps)
+                        ptx::mma_bf16_ta(cols + C::kO, pt + (uint32_t)kk * 8u, vd + n_step<D>(kk), idesc_o,
+                                         kk > 0 ? 1u : (uint32_t)(b > 0));
                 ptx::mma_commit(&sb->o_done[grp][buf]);
                 ptx::mma_commit(&sb->kv_empty[stage]);
                 return true;

@@ -17,18 +17,26 @@ __device__ __forceinline__ uint32_t op_offset(int r, int c, int rows) {
     if constexpr (D == 32) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
     return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-// Descriptor of a K-major operand (rows x D) at its k-th 16 channels.
+// Descriptor of a K-major operand (rows x D), and what its k-th 16 channels add
+// to it (the address field counts 16 bytes).
 template <int D>
-__device__ __forceinline__ uint64_t k_major(uint32_t tile, int kk, int rows) {
-    if constexpr (D == 32) return ptx::smem_desc(tile + kk * 32, 16, 512, ptx::kSwizzle64B);
-    return ptx::smem_desc(tile + (uint32_t)((kk >> 2) * rows * 128 + (kk & 3) * 32), 16, 1024, ptx::kSwizzle128B);
+__device__ __forceinline__ uint64_t k_major(uint32_t tile) {
+    if constexpr (D == 32) return ptx::smem_desc(tile, 16, 512, ptx::kSwizzle64B);
+    return ptx::smem_desc(tile, 16, 1024, ptx::kSwizzle128B);
 }
-// Descriptor of V (rows x D, channels the N axis) at its k-th 16 states.
 template <int D>
-__device__ __forceinline__ uint64_t v_operand(uint32_t tile, int kk, int rows) {
-    if constexpr (D == 32) return ptx::smem_desc(tile + kk * 1024, 16, 512, ptx::kSwizzle64B);
-    return ptx::smem_desc(tile + kk * 2048, rows * 128, 1024, ptx::kSwizzle128B);
+__device__ __forceinline__ constexpr uint32_t k_step(int kk, int rows) {
+    return D == 32 ? (uint32_t)kk * 2u : (uint32_t)((kk >> 2) * rows * 8 + (kk & 3) * 2);
 }
+// Descriptor of a tile whose rows are the inner axis (rows x D, channels the N
+// axis), and what its k-th 16 rows add.
+template <int D>
+__device__ __forceinline__ uint64_t n_major(uint32_t tile, int rows) {
+    if constexpr (D == 32) return ptx::smem_desc(tile, 16, 512, ptx::kSwizzle64B);
+    return ptx::smem_desc(tile, rows * 128, 1024, ptx::kSwizzle128B);
+}
+template <int D>
+__device__ __forceinline__ constexpr uint32_t n_step(int kk) { return (uint32_t)kk * (D == 32 ? 64u : 128u); }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int* abort, int* status) {
     for (uint32_t i = 0; i < kWait; ++i) {

@@ -14,12 +14,12 @@
 //
 // S and dP have two buffers (256 columns; the sums take 2 d of the others), so
 // that the products of the next block run under the exponentials of this one.
-// There is no maximum to agree on, so two threads share a row, 32 columns each.
-// Roles of the 12 warps: 0 issues S and dP, 1 the sums' products; 2 starts the
+// There is no maximum to agree on, so four threads share a row, 16 columns each.
+// Roles of the 20 warps: 0 issues S and dP, 1 the sums' products; 2 starts the
 // loads (TMA, or cp.async where no map can be made); 3 passes each landed tile
 // on, after it has zeroed the rows of masked or missing states (what is stored
 // there must not reach a product) and, for dK and dV, added the columns' log sums
-// and D; 4-7 and 8-11 are the rows' threads, left and right columns.
+// and D; 4-7, 8-11, 12-15, 16-19 are the rows' threads, by columns.
 // With two tiles of 128 rows a CTA, one buffer, and a thread a row (the first
 // form) a block's products and exponentials took turns: 4250 clocks for two
 // tiles, of which a row's threads waited 2360.
@@ -35,7 +35,8 @@ namespace {
 using namespace cross;
 
 constexpr int kCtrl = 4;
-constexpr int kThreads = 32 * (kCtrl + 8);
+constexpr int kShare = 4;   // threads of a row
+constexpr int kThreads = 32 * (kCtrl + 4 * kShare);
 constexpr int kStages = 4;  // at most
 constexpr int BN = 64;      // columns of a block
 
@@ -55,13 +56,13 @@ struct Cfg {
     static constexpr uint32_t kDp = 64, kAcc1 = 256, kAcc2 = 256 + D;
     static constexpr uint32_t kRow = 128u * D * 2u, kCol = (uint32_t)BN * D * 2u;
     static constexpr int kRing = D == 128 ? 3 : 4;
-    // rows [buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics (dQ: a row's sum of dS over its
-    // left, right columns), barriers
+    // rows [buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics (dQ: a row's sums of dS), barriers
     static constexpr uint32_t kOffCol = 2 * 2 * kRow;
     static constexpr uint32_t kOffStat = kOffCol + kRing * 2 * kCol;
-    static constexpr uint32_t kOffBar = kOffStat + kRing * 2 * BN * 4;
-    static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
-    static_assert(kSmem <= 227u * 1024u && kRing * 2 * BN >= 2 * 128, "shared memory");
+    static constexpr uint32_t kStat = kRing * 2 * BN * 4 > 128 * kShare * 4 ? kRing * 2 * BN * 4 : 128 * kShare * 4;
+    static constexpr uint32_t kOffBar = kOffStat + kStat;
+    static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers);  // (no room for an alignment's slack)
+    static_assert(kSmem <= 227u * 1024u, "shared memory");
 };
 
 struct BwdPlan {
@@ -165,9 +166,12 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
     using C = Cfg<D>;
     constexpr int kRing = C::kRing;
     constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
+    if (sbase & 1023u) {  // the swizzled tiles need what the declaration asks for
+        raise_status(status, kDevBounds);
+        return;
+    }
     Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -180,13 +184,13 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(&sb->r_land[x], 1);
             ptx::mbar_init(&sb->r_full[x], 1);
-            ptx::mbar_init(&sb->r_empty[x], STATES ? 1 : 1 + 256);  // the products; the reads of dO for D
+            ptx::mbar_init(&sb->r_empty[x], STATES ? 1 : 1 + 128 * kShare);  // the products; the reads of dO for D
             ptx::mbar_init(&sb->s_full[x], 1);
-            ptx::mbar_init(&sb->p_full[x], 256);
+            ptx::mbar_init(&sb->p_full[x], 128 * kShare);
             ptx::mbar_init(&sb->acc_done[x], 1);
             ptx::mbar_init(&sb->drain[x], 1);
         }
-        ptx::mbar_init(&sb->rest_full, 256);
+        ptx::mbar_init(&sb->rest_full, 128 * kShare);
         sb->abort = 0;
         ptx::mbar_init_fence();
     }
@@ -212,10 +216,11 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 const Unit x = unit_at<STATES>(g, p, u);
                 if (x.nb == 0) continue;
                 ok = wait_or_abort(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status);
-                const uint32_t r1 = row_tile(use);
+                const uint64_t r1 = k_major<D>(row_tile(use)), r2 = k_major<D>(row_tile(use) + C::kRow);
                 for (int b = 0; ok && b < x.nb; ++b, ++i) {
                     const int stage = i % kRing, buf = i & 1;
-                    const uint32_t c1 = col_tile(stage), cols = tmem + (uint32_t)buf * 128u;
+                    const uint32_t cols = tmem + (uint32_t)buf * 128u;
+                    const uint64_t c1 = k_major<D>(col_tile(stage)), c2 = k_major<D>(col_tile(stage) + C::kCol);
                     // the buffer holds the P and dS of two blocks ago until their products end
                     if (!wait_or_abort(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status) ||
                         (i >= 2 && !wait_or_abort(&sb->acc_done[buf], ((i >> 1) - 1) & 1, &sb->abort, status))) {
@@ -226,9 +231,8 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<STATES>(x, b), false, false);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        ptx::mma_bf16(cols, k_major<D>(r1, kk, 128), k_major<D>(c1, kk, BN), idesc, kk);
-                        ptx::mma_bf16(cols + C::kDp, k_major<D>(r1 + C::kRow, kk, 128), k_major<D>(c1 + C::kCol, kk, BN),
-                                      idesc, kk);
+                        ptx::mma_bf16(cols, r1 + k_step<D>(kk, 128), c1 + k_step<D>(kk, BN), idesc, kk);
+                        ptx::mma_bf16(cols + C::kDp, r2 + k_step<D>(kk, 128), c2 + k_step<D>(kk, BN), idesc, kk);
                     }
                     ptx::mma_commit(&sb->s_full[buf]);
                     if (b == x.nb - 1) ptx::mma_commit(&sb->r_empty[use & 1]);
@@ -249,7 +253,8 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 const Unit x = unit_at<STATES>(g, p, u);
                 for (int b = 0; b < x.nb; ++b, ++i) {
                     const int stage = i % kRing, buf = i & 1;
-                    const uint32_t c1 = col_tile(stage), c2 = STATES ? c1 + C::kCol : c1;
+                    const uint64_t c1 = n_major<D>(col_tile(stage), BN);
+                    const uint64_t c2 = STATES ? n_major<D>(col_tile(stage) + C::kCol, BN) : c1;
                     const uint32_t cols = tmem + (uint32_t)buf * 128u;
                     if (!wait_or_abort(&sb->p_full[buf], (i >> 1) & 1, &sb->abort, status)) {
                         ok = false;
@@ -257,11 +262,13 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     }
                     ptx::tc_fence_after();
                     const int steps = block_cols<STATES>(x, b) >> 4;
-                    for (int kk = 0; kk < steps; ++kk) {  // 16 columns: of the left half for kk < 2
-                        const uint32_t a = cols + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8);
-                        ptx::mma_bf16_ta(tmem + C::kAcc1, a + C::kDp, v_operand<D>(c1, kk, BN), idesc, b > 0 || kk > 0);
-                        ptx::mma_bf16_ta(tmem + C::kAcc2, a, v_operand<D>(c2, kk, BN), idesc, b > 0 || kk > 0);
-                    }
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        if (kk < steps) {
+                            const uint32_t a = cols + (uint32_t)kk * 16u, more = kk > 0 ? 1u : (uint32_t)(b > 0);
+                            ptx::mma_bf16_ta(tmem + C::kAcc1, a + C::kDp, c1 + n_step<D>(kk), idesc, more);
+                            ptx::mma_bf16_ta(tmem + C::kAcc2, a, c2 + n_step<D>(kk), idesc, more);
+                        }
                     ptx::mma_commit(&sb->acc_done[buf]);
                     ptx::mma_commit(&sb->c_empty[stage]);
                 }
@@ -383,7 +390,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         }
     } else {
         // ---------------------------------------------------- P, dS and the epilogue
-        const int half = (warp - kCtrl) >> 2, qd = warp & 3;
+        const int part = (warp - kCtrl) >> 2, qd = warp & 3;  // columns 16 part .. + 15
         const int row = 32 * qd + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16);
         const float c2 = g.scale * kLog2e;
@@ -428,20 +435,22 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     break;
                 }
                 ptx::tc_fence_after();
-                const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN + half * 32;
-                if (STATES || block_cols<STATES>(x, b) > half * 32) {
-                    uint32_t s[32], dp[32];
-                    ptx::tmem_load_pair(cols + half * 32, cols + C::kDp + half * 32, s, dp);
-                    const uint32_t w = STATES ? 0xffffffffu : sb->words[stage][half];
-                    uint32_t pp[16], pd[16];
+                const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN + part * 16;
+                if (STATES || block_cols<STATES>(x, b) > part * 16) {
+                    uint32_t s[16], dp[16];
+                    ptx::tmem_load_pair(cols + part * 16, cols + C::kDp + part * 16, s, dp);
+                    const uint32_t w = STATES ? 0xffffu : (sb->words[stage][part >> 1] >> ((part & 1) * 16)) & 0xffffu;
+                    uint32_t pp[8], pd[8];
                     auto form = [&](bool masked) {
                         const uint64_t noff2 = ptx::pack_f32x2(noff, noff), nd2 = ptx::pack_f32x2(nd, nd);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < 8; ++e) {
                             uint64_t no = noff2, dd = nd2;
                             if constexpr (STATES) {
-                                no = *reinterpret_cast<const uint64_t*>(stat + 2 * e);
-                                dd = *reinterpret_cast<const uint64_t*>(stat + BN + 2 * e);
+                                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(stat + (e & ~1) * 2);
+                                const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(stat + BN + (e & ~1) * 2);
+                                no = e & 1 ? a.y : a.x;
+                                dd = e & 1 ? z.y : z.x;
                             }
                             float lo, hi, dlo, dhi;
                             ptx::unpack_f32x2(
@@ -465,11 +474,11 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                             pd[e] = ptx::pack_bf16x2(dlo, dhi);
                         }
                     };
-                    if (STATES || w == 0xffffffffu) form(false);
+                    if (STATES || w == 0xffffu) form(false);
                     else form(true);
-                    // each side's over the first 16 of the scores that it has read itself
-                    ptx::tmem_st16(cols + half * 32, pp);
-                    ptx::tmem_st16(cols + C::kDp + half * 32, pd);
+                    // over the first 8 of the 16 scores that this thread has read
+                    ptx::tmem_st8(cols + part * 16, pp);
+                    ptx::tmem_st8(cols + C::kDp + part * 16, pd);
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
@@ -491,30 +500,26 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     float lo, hi;
                     ptx::unpack_f32x2(rest2, lo, hi);
                     float* rests = reinterpret_cast<float*>(smem + C::kOffStat);
-                    rests[half * 128 + row] = lo + hi;
+                    rests[part * 128 + row] = lo + hi;
                     ptx::mbar_arrive(&sb->rest_full);
                     if (!warp_wait(&sb->rest_full, use & 1, &sb->abort, status)) break;
-                    rest = rests[row] + rests[128 + row];
+#pragma unroll
+                    for (int y = 0; y < kShare; ++y) rest += rests[y * 128 + row];
                 }
                 if (in) {
                     at = cross_o_offset(g, x.b, x.j, r0);
-                    if (half == 0) delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
+                    if (part == 0) delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
                 }
             }
             const size_t elems = (size_t)g.B * g.Lk * g.kv_heads * D;
 #pragma unroll 1
-            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-                uint32_t a1[16], a2[16];
-                if (x.nb > 0) {
-                    ptx::tmem_ld16(lanes + C::kAcc1 + c, a1);
-                    ptx::tmem_ld16(lanes + C::kAcc2 + c, a2);
-                    ptx::tmem_wait16(a1);
-                    ptx::tmem_wait16(a2);
-                }
+            for (int c = part * (D / kShare); c < (part + 1) * (D / kShare); c += 8) {
+                uint32_t a1[8], a2[8];
+                if (x.nb > 0) ptx::tmem_load_pair(lanes + C::kAcc1 + c, lanes + C::kAcc2 + c, a1, a2);
                 if (!in) continue;
-                float f1[16], f2[16];
+                float f1[8], f2[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     f1[e] = live ? __uint_as_float(a1[e]) : 0.f;
                     f2[e] = live ? __uint_as_float(a2[e]) : 0.f;
                     if (!STATES) f1[e] = fmaf(-rest, f2[e], f1[e]);
@@ -523,21 +528,18 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 if (STATES && p.splits > 1) {
                     float* out = parts + (size_t)x.split * 2 * elems + at + c;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
+                    for (int e = 0; e < 8; e += 4) {
                         *reinterpret_cast<float4*>(out + e) = make_float4(f1[e], f1[e + 1], f1[e + 2], f1[e + 3]);
                         *reinterpret_cast<float4*>(out + elems + e) = make_float4(f2[e], f2[e + 1], f2[e + 2], f2[e + 3]);
                     }
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        *reinterpret_cast<uint4*>(out1 + at + c + e) =
-                            make_uint4(ptx::pack_bf16x2(f1[e], f1[e + 1]), ptx::pack_bf16x2(f1[e + 2], f1[e + 3]),
-                                       ptx::pack_bf16x2(f1[e + 4], f1[e + 5]), ptx::pack_bf16x2(f1[e + 6], f1[e + 7]));
-                        if (STATES)
-                            *reinterpret_cast<uint4*>(out2 + at + c + e) =
-                                make_uint4(ptx::pack_bf16x2(f2[e], f2[e + 1]), ptx::pack_bf16x2(f2[e + 2], f2[e + 3]),
-                                           ptx::pack_bf16x2(f2[e + 4], f2[e + 5]), ptx::pack_bf16x2(f2[e + 6], f2[e + 7]));
-                    }
+                    *reinterpret_cast<uint4*>(out1 + at + c) =
+                        make_uint4(ptx::pack_bf16x2(f1[0], f1[1]), ptx::pack_bf16x2(f1[2], f1[3]),
+                                   ptx::pack_bf16x2(f1[4], f1[5]), ptx::pack_bf16x2(f1[6], f1[7]));
+                    if (STATES)
+                        *reinterpret_cast<uint4*>(out2 + at + c) =
+                            make_uint4(ptx::pack_bf16x2(f2[0], f2[1]), ptx::pack_bf16x2(f2[2], f2[3]),
+                                       ptx::pack_bf16x2(f2[4], f2[5]), ptx::pack_bf16x2(f2[6], f2[7]));
                 }
             }
             if (x.nb > 0) ++use;

@@ -11,11 +11,11 @@
 // is the same, and l, in fp32, uses the same offset), so that the common
 // block costs no pass over O.
 //
-// Roles of the 11 warps, one CTA on an SM: 0, 1 issue the products of tile 0, 1;
-// 2 loads the blocks of K and V, and both tiles' Q (double-buffered), by TMA, a
-// block with a masked state, or past the entry's last, by 16-byte cp.async that
-// fill the missing rows with zeros, so that what is stored there never reaches a
-// product; 3-6, 7-10 are the tiles' softmax.  For d <= 64 the next S is issued as
+// Roles of the 12 warps, one CTA on an SM: 0, 1 issue the products of tile 0, 1;
+// 2 starts the loads of K and V, and of both tiles' Q (double-buffered), by TMA
+// (cp.async where no map can be made); 3 passes each landed block on, after it has
+// zeroed V's rows of masked or missing states, so that what is stored there never
+// reaches a product; 4-7, 8-11 are the tiles' softmax. For d <= 64 the next S is issued as
 // soon as the scores are in registers, under the exponentials.  For d = 128 the
 // columns do not suffice for a P of its own: P takes its S's, and S has two
 // buffers, so that the next S is there before this softmax ends.
@@ -37,18 +37,18 @@ namespace {
 
 using namespace cross;
 
-constexpr int kCtrl = 3;
+constexpr int kCtrl = 4;
 constexpr int kThreads = 32 * (kCtrl + 8);
 constexpr int kStages = 4;  // at most
 constexpr float kGrow = 8.f;  // powers of two a maximum may grow by before O is rescaled
 
 struct Barriers {
-    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t kv_land[kStages], kv_full[kStages], kv_empty[kStages];
     uint64_t q_full[2][2], q_empty[2][2];
     // [tile][buffer of the block]
     uint64_t s_full[2][2], s_free[2][2], p_full[2][2], o_done[2][2];
     uint64_t drain[2];
-    uint32_t words[kStages][4];  // the block's valid states, where a mask says which
+    uint32_t words[kStages][4];  // the block's valid states
     uint32_t tmem;
     int abort;
 };
@@ -117,6 +117,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(&sb->kv_land[i], 1);
             ptx::mbar_init(&sb->kv_full[i], 1);
             ptx::mbar_init(&sb->kv_empty[i], 2);
         }
@@ -200,7 +201,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             ptx::mbar_wait(&sb->drain[grp], 0, kWait);
         }
         __syncwarp();
-    } else if (warp < kCtrl) {
+    } else if (warp == 2) {
         // ------------------------------------------------------------------ loads
         constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
         if (lane == 0) {
@@ -230,14 +231,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                                              g.q_batch ? x.b : 0, full);
                     }
                 } else {
-#pragma unroll 4
-                    for (int e = lane; e < 128 * (D / 8); e += 32) {
-                        const int r = e / (D / 8), c = e % (D / 8);
-                        const bool on = row0 + r < g.rows;
-                        ptx::cp_async16_zfill(qt + op_offset<D>(r, c, 128),
-                                              on ? q + cross_q_offset(g, x.b, x.j, row0 + r) + c * 8 : q,
-                                              on ? 16u : 0u);
-                    }
+                    tc_load_queries<D>(qt, q, false, g, x.b, x.j, row0, 128, lane);
                     ptx::cp_async_wait_all();
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
@@ -248,57 +242,59 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const __nv_bfloat16* vbase = v + (size_t)x.b * g.v_batch + (size_t)x.j * D;
             for (int b = 0; ok && b < x.nb; ++b, ++i) {
                 const int stage = i % kRing, key0 = (x.t0 + b) * BN;
-                uint32_t w[BN / 32], every = 0xffffffffu;
-#pragma unroll
-                for (int h = 0; h < BN / 32; ++h) {
-                    const int key = key0 + h * 32 + lane;
-                    w[h] = __ballot_sync(0xffffffffu,
-                                         key < x.n && (!g.kv_mask || __ldcg(g.kv_mask + (size_t)x.b * g.Lk + key) != 0));
-                    every &= w[h];
-                }
+                uint32_t w[BN / 32];
+                valid_words(g, x.b, x.n, key0, lane, w);
                 if (i >= kRing && !warp_wait(&sb->kv_empty[stage], ((i / kRing) - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
                 const uint32_t kt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile;
-                uint64_t* full = &sb->kv_full[stage];
-                if (lane == 0 && g.kv_mask) {
+                uint64_t* land = &sb->kv_land[stage];
+                if (lane == 0) {
 #pragma unroll
                     for (int h = 0; h < BN / 32; ++h) sb->words[stage][h] = w[h];
                 }
-                if (p.tma_kv && every == 0xffffffffu) {
+                if (p.tma_kv) {
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(full, 2u * C::kKvTile);
+                        ptx::mbar_arrive_expect_tx(land, 2u * C::kKvTile);
 #pragma unroll
                         for (int c = 0; c < kPanels; ++c) {
                             ptx::tma_load_4d(kt + (uint32_t)c * BN * 128u, &tk, c * 64, x.j, key0, g.k_batch ? x.b : 0,
-                                             full);
+                                             land);
                             ptx::tma_load_4d(kt + C::kKvTile + (uint32_t)c * BN * 128u, &tv, c * 64, x.j, key0,
-                                             g.v_batch ? x.b : 0, full);
+                                             g.v_batch ? x.b : 0, land);
                         }
                     }
                 } else {
-                    const int rows = block_cols<BN>(x.n, x.t0 + b);  // no product reads past them
-#pragma unroll 4
-                    for (int e = lane; e < rows * (D / 8); e += 32) {
-                        const int r = e / (D / 8), c = e % (D / 8);
-                        uint32_t word = w[0];
-#pragma unroll
-                        for (int h = 1; h < BN / 32; ++h) word = r >= h * 32 ? w[h] : word;
-                        const bool on = (word >> (r & 31)) & 1u;
-                        const uint32_t at = op_offset<D>(r, c, BN);
-                        ptx::cp_async16_zfill(kt + at, on ? kbase + (size_t)(key0 + r) * g.k_row + c * 8 : k,
-                                              on ? 16u : 0u);
-                        ptx::cp_async16_zfill(kt + C::kKvTile + at,
-                                              on ? vbase + (size_t)(key0 + r) * g.v_row + c * 8 : v, on ? 16u : 0u);
-                    }
+                    tc_load_states<D>(kt, kbase, g.k_row, key0, x.n, BN, lane);
+                    tc_load_states<D>(kt + C::kKvTile, vbase, g.v_row, key0, x.n, BN, lane);
                     ptx::cp_async_wait_all();
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(full);
+                    if (lane == 0) ptx::mbar_arrive(land);
                 }
             }
             ++use;
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------- landed blocks, passed to the products
+        int i = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
+            const Unit x = unit_at<BN>(g, p, u);
+            for (int b = 0; b < x.nb; ++b, ++i) {
+                const int stage = i % kRing;
+                if (!warp_wait(&sb->kv_land[stage], (i / kRing) & 1, &sb->abort, status)) {
+                    ok = false;
+                    break;
+                }
+                // K's rows need not be cleared: their scores are replaced, and no sum runs over them
+                const uint32_t vt = sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile;
+                clear_states<D, BN / 32, 1>(vt, 0u, sb->words[stage], lane);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sb->kv_full[stage]);
+            }
         }
     } else {
         // ------------------------------------------------------ softmax + epilogue
@@ -331,16 +327,14 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 }
                 const int left = x.n - (x.t0 + b) * BN;
                 if (g.kv_mask || left < BN) {
-                    // (the block's loads are done; the wait makes the loader's words visible)
-                    if (g.kv_mask && !warp_wait(&sb->kv_full[i % kRing], (i / kRing) & 1, &sb->abort, status)) {
+                    // (the block has been passed on; the wait makes its words visible)
+                    if (!warp_wait(&sb->kv_full[i % kRing], (i / kRing) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
                     for (int h = 0; h < BN / 32; ++h) {
-                        const int rest = left - h * 32;
-                        const uint32_t w = g.kv_mask ? sb->words[i % kRing][h]
-                                                     : (rest >= 32 ? 0xffffffffu : rest <= 0 ? 0u : (1u << rest) - 1u);
+                        const uint32_t w = sb->words[i % kRing][h];
                         if (w != 0xffffffffu) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)

@@ -46,6 +46,7 @@ struct Barriers {
     uint64_t s_full[2], p_full[2], acc_done[2];  // [buffer]
     uint64_t rest_full, drain[2];
     uint32_t words[kStages][2];  // dQ: the block's valid states
+    uint32_t row_words[2][4];    // dK, dV: the tile's
     uint32_t tmem;
     int abort;
 };
@@ -101,57 +102,6 @@ __device__ __forceinline__ Unit unit_at(const CrossGeom& g, const BwdPlan& p, in
 template <bool STATES>
 __device__ __forceinline__ int block_cols(const Unit& x, int b) {
     return STATES ? BN : (min(BN, x.n - (x.t0 + b) * BN) + 15) & ~15;
-}
-
-// ``rows`` rows of queries (dense: O's layout) from row0; past the last: zeros.
-template <int D>
-__device__ __forceinline__ void load_queries(uint32_t dst, const __nv_bfloat16* base, bool dense, const CrossGeom& g,
-                                             int b, int j, int row0, int rows, int lane) {
-#pragma unroll 4
-    for (int e = lane; e < rows * (D / 8); e += 32) {
-        const int r = e / (D / 8), c = e % (D / 8);
-        const bool on = row0 + r < g.rows;
-        const size_t off = !on ? 0 : dense ? cross_o_offset(g, b, j, row0 + r) : cross_q_offset(g, b, j, row0 + r);
-        ptx::cp_async16_zfill(dst + op_offset<D>(r, c, rows), base + off + (on ? c * 8 : 0), on ? 16u : 0u);
-    }
-}
-
-// ``rows`` rows of states from key0, those from ``end`` on not read.
-template <int D>
-__device__ __forceinline__ void load_states(uint32_t dst, const __nv_bfloat16* base, long long step, int key0, int end,
-                                            int rows, int lane) {
-#pragma unroll 4
-    for (int e = lane; e < rows * (D / 8); e += 32) {
-        const int r = e / (D / 8), c = e % (D / 8);
-        const bool on = key0 + r < end;
-        ptx::cp_async16_zfill(dst + op_offset<D>(r, c, rows), on ? base + (size_t)(key0 + r) * step + c * 8 : base,
-                              on ? 16u : 0u);
-    }
-}
-
-// Zeros in the rows of two tiles (``second`` bytes apart) whose bit in w is off.
-template <int D, int W>
-__device__ __forceinline__ void clear_states(uint32_t dst, uint32_t second, const uint32_t (&w)[W], int lane) {
-    for (int h = 0; h < W; ++h)
-        for (uint32_t off = ~w[h]; off != 0u; off &= off - 1u) {
-            const int r = h * 32 + __ffs(off) - 1;
-            for (int c = lane; c < D / 4; c += 32)
-                ptx::st_shared_v4(dst + (c >= D / 8 ? second : 0u) + op_offset<D>(r, c & (D / 8 - 1), W * 32), 0u, 0u, 0u,
-                                  0u);
-        }
-}
-
-// Validity of 32 W states from key0 as bits; true if all are.
-template <int W>
-__device__ __forceinline__ bool valid_words(const CrossGeom& g, int b, int n, int key0, int lane, uint32_t (&w)[W]) {
-    uint32_t every = 0xffffffffu;
-#pragma unroll
-    for (int h = 0; h < W; ++h) {
-        const int key = key0 + h * 32 + lane;
-        w[h] = __ballot_sync(0xffffffffu, key < n && (!g.kv_mask || __ldcg(g.kv_mask + (size_t)b * g.Lk + key) != 0));
-        every &= w[h];
-    }
-    return every == 0xffffffffu;
 }
 
 // STATES: the rows are states (dK, dV), the columns queries; else the rows are
@@ -306,12 +256,12 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     }
                 } else {
                     if (states) {
-                        load_states<D>(dst, k + (size_t)x.b * g.k_batch + (size_t)x.j * D, g.k_row, r0, x.n, rows, lane);
-                        load_states<D>(dst + second, v + (size_t)x.b * g.v_batch + (size_t)x.j * D, g.v_row, r0, x.n,
+                        tc_load_states<D>(dst, k + (size_t)x.b * g.k_batch + (size_t)x.j * D, g.k_row, r0, x.n, rows, lane);
+                        tc_load_states<D>(dst + second, v + (size_t)x.b * g.v_batch + (size_t)x.j * D, g.v_row, r0, x.n,
                                        rows, lane);
                     } else {
-                        load_queries<D>(dst, q, false, g, x.b, x.j, r0, rows, lane);
-                        load_queries<D>(dst + second, go, true, g, x.b, x.j, r0, rows, lane);
+                        tc_load_queries<D>(dst, q, false, g, x.b, x.j, r0, rows, lane);
+                        tc_load_queries<D>(dst + second, go, true, g, x.b, x.j, r0, rows, lane);
                     }
                     ptx::cp_async_wait_all();
                     ptx::fence_proxy_async_smem();
@@ -319,13 +269,24 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     if (lane == 0) ptx::mbar_arrive(land);
                 }
             };
+            uint32_t wr[4], w[2];
+            if (STATES) valid_words(g, x.b, x.n, x.row0, lane, wr);
             if (use >= 2 && !warp_wait(&sb->r_empty[use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) break;
+            if (STATES && lane == 0) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) sb->row_words[use & 1][h] = wr[h];
+            }
             load(row_tile(use), C::kRow, STATES, x.row0, 128, p.tma_r, &tr1, &tr2, &sb->r_land[use & 1]);
             for (int b = 0; b < x.nb; ++b, ++i) {
                 const int stage = i % kRing;
+                if (!STATES) valid_words(g, x.b, x.n, (x.t0 + b) * BN, lane, w);
                 if (i >= kRing && !warp_wait(&sb->c_empty[stage], ((i / kRing) - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
+                }
+                if (!STATES && lane == 0) {
+                    sb->words[stage][0] = w[0];
+                    sb->words[stage][1] = w[1];
                 }
                 load(col_tile(stage), C::kCol, !STATES, (x.t0 + b) * BN, BN, p.tma_c, &tc1, &tc2, &sb->c_land[stage]);
             }
@@ -343,29 +304,21 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(full);
             };
-            uint32_t wr[4];
-            bool whole = true;
-            if (STATES) whole = valid_words(g, x.b, x.n, x.row0, lane, wr);
             if (!warp_wait(&sb->r_land[use & 1], (use >> 1) & 1, &sb->abort, status)) break;
-            if (STATES && !whole) clear_states<D>(row_tile(use), C::kRow, wr, lane);
+            if (STATES) clear_states<D, 4>(row_tile(use), C::kRow, sb->row_words[use & 1], lane);
             pass(&sb->r_full[use & 1]);
             float st[4];  // STATES: this lane's share of a block's log sums (2) and D (2), read a block ahead
-            uint32_t w[2];
             auto ahead = [&](int b) {
-                if constexpr (STATES) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = (x.t0 + b) * BN + h * 32 + lane;
-                        const bool in = b < x.nb && r < g.rows;
-                        const size_t at = in ? cross_lse_offset(g, x.b, x.j, r) : 0;
-                        st[h] = in ? __ldcg(lse + at) : -INFINITY;
-                        st[2 + h] = in ? __ldcg(delta + at) : 0.f;
-                    }
-                } else {
-                    whole = b >= x.nb || valid_words(g, x.b, x.n, (x.t0 + b) * BN, lane, w);
+                for (int h = 0; h < 2; ++h) {
+                    const int r = (x.t0 + b) * BN + h * 32 + lane;
+                    const bool in = b < x.nb && r < g.rows;
+                    const size_t at = in ? cross_lse_offset(g, x.b, x.j, r) : 0;
+                    st[h] = in ? __ldcg(lse + at) : -INFINITY;
+                    st[2 + h] = in ? __ldcg(delta + at) : 0.f;
                 }
             };
-            ahead(0);
+            if (STATES) ahead(0);
             for (int b = 0; b < x.nb; ++b, ++i) {
                 const int stage = i % kRing;
                 if (!warp_wait(&sb->c_land[stage], (i / kRing) & 1, &sb->abort, status)) {
@@ -380,11 +333,10 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                         stat[BN + h * 32 + lane] = -st[2 + h];
                     }
                 } else {
-                    if (lane < 2) sb->words[stage][lane] = w[lane];
-                    if (!whole) clear_states<D>(col_tile(stage), C::kCol, w, lane);
+                    clear_states<D, 2>(col_tile(stage), C::kCol, sb->words[stage], lane);
                 }
                 pass(&sb->c_full[stage]);
-                ahead(b + 1);
+                if (STATES) ahead(b + 1);
             }
             ++use;
         }

@@ -59,6 +59,10 @@ size_t cross_forward_part_rows(const CrossGeom& g, const CrossPlan& p);  // 0 wi
 
 bra_status cross_forward_bf16(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,
                               void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream);
+// The form for few states (bf16).
+bool cross_short_covers(const CrossGeom& g);
+bra_status cross_forward_short(const CrossGeom& g, const void* q, const void* k, const void* v, void* o, float* lse,
+                               cudaStream_t stream);
 // The form for many rows (tcgen05); covers() says from how many on it is taken.
 bool cross_tc_covers(const CrossGeom& g);
 int cross_tc_rows();

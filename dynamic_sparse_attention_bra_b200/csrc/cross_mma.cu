@@ -387,6 +387,7 @@ size_t cross_forward_part_rows(const CrossGeom& g, const CrossPlan& p) {
 
 bra_status cross_forward_bf16(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,
                               void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream) {
+    if (cross_short_covers(g)) return cross_forward_short(g, q, k, v, o, lse, stream);
     const bra_status rc = cross_tc_covers(g) ? cross_forward_tc(g, p.splits, q, k, v, o, lse, parts, status, stream)
                           : g.d == 32   ? launch_d<32>(g, p.splits, q, k, v, o, lse, parts, stream)
                           : g.d == 64 ? launch_d<64>(g, p.splits, q, k, v, o, lse, parts, stream)

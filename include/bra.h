@@ -336,8 +336,9 @@ size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
  *   lse        device fp32 [B, heads, Lq], written (the backward needs it), or NULL
  *   workspace  device, bra_cross_workspace_bytes(shape) bytes
  * bf16: products on tensor cores with fp32 sums, the softmax in fp32, P
- * rounded once to bf16 as an operand, O rounded once.  fp32: CUDA cores, fp32
- * throughout.  The same inputs give the same bits.
+ * rounded once to bf16 as an operand, O rounded once.  fp32: each product of
+ * two factors as three tf32 products of their parts (relative error 2^-20),
+ * sums and softmax in fp32.  The same inputs give the same bits.
  * Errors: BRA_ERR_INVALID_ARG, BRA_ERR_UNSUPPORTED (another d, or past the
  * limits), BRA_ERR_CUDA.
  */

@@ -1,6 +1,7 @@
 // Cross attention to an encoder's states: geometry and launchers (internal).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 
 #include "../../include/bra.h"
@@ -40,6 +41,21 @@ __device__ __forceinline__ size_t cross_o_offset(const CrossGeom& g, int b, int 
 __device__ __forceinline__ size_t cross_lse_offset(const CrossGeom& g, int b, int j, int r) {
     const int t = r / g.rep, hh = r - t * g.rep;
     return ((size_t)b * g.heads + (size_t)(j * g.rep + hh)) * g.Lq + t;
+}
+
+// Allows ``kernel`` its dynamic shared memory, once for each device (a launch
+// attribute; setting it on every call would cost as much as a third of a launch).
+template <auto kernel>
+inline bool allow_shared(uint32_t bytes) {
+    static std::atomic<uint64_t> done[4];  // a bit for each of 256 devices
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done[dev >> 6].load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return false;
+    done[dev >> 6].fetch_or(bit, std::memory_order_release);
+    return true;
 }
 
 // Partial results of a key split: rows x d unnormalised sums, then (maximum in

@@ -420,10 +420,7 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
                     const float* lse, const void* go, void* dq, void* dk, void* dv, float* delta, float* parts,
                     cudaStream_t stream) {
     using T = __nv_bfloat16;
-    if (cudaFuncSetAttribute(bra_cross_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dq_smem<D>()) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(bra_cross_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)dkv_smem<D>()) != cudaSuccess)
+    if (!allow_shared<bra_cross_dq_kernel<D>>(dq_smem<D>()) || !allow_shared<bra_cross_dkv_kernel<D>>(dkv_smem<D>()))
         return BRA_ERR_CUDA;
     const int row_tiles = (g.rows + 63) / 64, key_tiles = (g.Lk + 63) / 64;
     const long long grid_q = (long long)row_tiles * g.kv_heads * g.B;

@@ -305,9 +305,11 @@ bra_cross_join_kernel(CrossParts parts, T* __restrict__ o, float* __restrict__ l
     allow_dependents();
     if (at >= rows_all) return;
     float m = -INFINITY, l = 0.f;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) m = fmaxf(m, __ldcg(parts.ml + s * rows_all + at).x);
     const float mu = m == -INFINITY ? 0.f : m;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
         const float2 ml = __ldcg(parts.ml + s * rows_all + at);
         const float4 y = __ldcg(reinterpret_cast<const float4*>(parts.o + (size_t)(s * rows_all + at) * g.d + c));
@@ -335,8 +337,7 @@ bra_status launch(const CrossGeom& g, int splits, const void* q, const void* k, 
                   CrossParts parts, cudaStream_t stream) {
     using S = Smem<D, WM, WN, MI>;
     auto* kernel = bra_cross_mma_kernel<D, WM, WN, MI>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes) != cudaSuccess)
-        return BRA_ERR_CUDA;
+    if (!allow_shared<bra_cross_mma_kernel<D, WM, WN, MI>>(S::kBytes)) return BRA_ERR_CUDA;
     const int row_tiles = (g.rows + S::kRows - 1) / S::kRows;
     const long long grid = (long long)row_tiles * splits * g.kv_heads * g.B;
     if (grid > 0x7fffffffLL) return BRA_ERR_UNSUPPORTED;
@@ -364,7 +365,9 @@ int rows_per_cta(const CrossGeom& g, bool bf16) {
 }  // namespace
 
 // The states are split where (row tiles x state heads x entries) leave SMs
-// idle: enough parts for four CTAs on each SM, none below 256 states.
+// idle: enough parts for eight small CTAs on each SM (of which four run: entries
+// of different lengths even out; four parts: 81 us where eight take 76, sixteen
+// 82: 16 entries of up to 16384 states, 8 heads of 64), none below 256 states.
 CrossPlan cross_forward_plan(const CrossGeom& g, bool bf16) {
     CrossPlan p{1};
     const int sms = sm_count();
@@ -374,7 +377,7 @@ CrossPlan cross_forward_plan(const CrossGeom& g, bool bf16) {
     // the many-row form has one CTA of 256 rows on an SM; the others several small ones
     const bool tc = bf16 && cross_tc_covers(g);
     if (ctas <= 0 || ctas >= (tc ? 1LL : 2LL) * sms) return p;
-    long long s = (tc ? 1LL : 4LL) * sms / ctas;
+    long long s = (tc ? 1LL : 8LL) * sms / ctas;
     const long long most = g.Lk / (tc ? 512 : 256);
     if (s > most) s = most;
     p.splits = s < 1 ? 1 : (int)s;

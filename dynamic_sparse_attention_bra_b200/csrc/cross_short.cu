@@ -283,10 +283,7 @@ bra_status launch_d(const CrossGeom& g, const void* q, const void* k, const void
     const long long tiles = (long long)row_tiles * g.kv_heads * g.B;
     const int sms = sm_count();
     if (sms <= 0) return BRA_ERR_CUDA;
-    if (bytes > 48u * 1024u &&
-        cudaFuncSetAttribute(bra_cross_short_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxStates * D * 4) != cudaSuccess)
-        return BRA_ERR_CUDA;
+    if (!allow_shared<bra_cross_short_kernel<D>>(kMaxStates * D * 4)) return BRA_ERR_CUDA;
     // two CTAs an SM; fewer where the tiles do not give each warp one
     const long long most = (long long)kCtas * sms, few = (tiles + kWarps - 1) / kWarps;
     const int grid = (int)(few < most ? few : most);

@@ -470,9 +470,7 @@ template <int D>
 bra_status launch_d(const CrossGeom& g, const TcPlan& plan, int grid, const void* q, const void* k, const void* v,
                     void* o, float* lse, CrossParts parts, int* status, cudaStream_t stream) {
     using C = Cfg<D>;
-    if (cudaFuncSetAttribute(bra_cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
-        cudaSuccess)
-        return BRA_ERR_CUDA;
+    if (!allow_shared<bra_cross_tc_kernel<D>>(C::kSmem)) return BRA_ERR_CUDA;
     TcPlan p = plan;
     CUtensorMap tq = {}, tk = {}, tv = {};
     // a Q tile is 128 / rep tokens; where rep does not divide it, and where a step is too long, cp.async

@@ -13,13 +13,14 @@
 // whose sums stay in TMEM over all blocks.
 //
 // S and dP have two buffers (256 columns; the sums take 2 d of the others), so
-// that the products of the next block run under the exponentials of this one.
-// There is no maximum to agree on, so four threads share a row, 16 columns each.
-// Roles of the 20 warps: 0 issues S and dP, 1 the sums' products; 2 starts the
+// that the products of the next block run under the exponentials of this one (d =
+// 32: one buffer, and two CTAs on an SM, which also hide the ends of short units).
+// There is no maximum to agree on, so four (two) threads share a row, in parts of
+// 16 columns.  Roles of the warps: 0 issues S and dP, 1 the sums' products; 2 starts the
 // loads (TMA, or cp.async where no map can be made); 3 passes each landed tile
 // on, after it has zeroed the rows of masked or missing states (what is stored
 // there must not reach a product) and, for dK and dV, added the columns' log sums
-// and D; 4-7, 8-11, 12-15, 16-19 are the rows' threads, by columns.
+// and D; from 4 on, four warps for each share of the columns, the rows' threads.
 // With two tiles of 128 rows a CTA, one buffer, and a thread a row (the first
 // form) a block's products and exponentials took turns: 4250 clocks for two
 // tiles, of which a row's threads waited 2360.
@@ -35,8 +36,7 @@ namespace {
 using namespace cross;
 
 constexpr int kCtrl = 4;
-constexpr int kShare = 4;   // threads of a row
-constexpr int kThreads = 32 * (kCtrl + 4 * kShare);
+constexpr int kParts = 4;   // 16-column parts of a block
 constexpr int kStages = 4;  // at most
 constexpr int BN = 64;      // columns of a block
 
@@ -53,8 +53,13 @@ struct Barriers {
 
 template <int D>
 struct Cfg {
-    // TMEM: buffer x: S at 128 x, dP at 128 x + 64 (P and dS over their first halves); sums
-    static constexpr uint32_t kDp = 64, kAcc1 = 256, kAcc2 = 256 + D;
+    static constexpr int kCtas = D == 32 ? 2 : 1;   // on an SM
+    static constexpr int kBufs = D == 32 ? 1 : 2;   // of S and dP
+    static constexpr int kShare = D == 32 ? 2 : 4;  // threads of a row
+    static constexpr int kThreads = 32 * (kCtrl + 4 * kShare);
+    // TMEM: buffer x: S at 128 x, dP at 128 x + 64 (P and dS over them); sums
+    static constexpr uint32_t kCols = D == 32 ? 256 : 512;
+    static constexpr uint32_t kDp = 64, kAcc1 = 128 * kBufs, kAcc2 = 128 * kBufs + D;
     static constexpr uint32_t kRow = 128u * D * 2u, kCol = (uint32_t)BN * D * 2u;
     static constexpr int kRing = D == 128 ? 3 : 4;
     // rows [buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics (dQ: a row's sums of dS), barriers
@@ -107,14 +112,14 @@ __device__ __forceinline__ int block_cols(const Unit& x, int b) {
 // STATES: the rows are states (dK, dV), the columns queries; else the rows are
 // queries (dQ), the columns states.
 template <int D, bool STATES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __grid_constant__ CUtensorMap tr2,
                              const __grid_constant__ CUtensorMap tc1, const __grid_constant__ CUtensorMap tc2,
                              const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                              const __nv_bfloat16* o, const float* lse, const __nv_bfloat16* go, __nv_bfloat16* out1,
                              __nv_bfloat16* out2, float* delta, float* parts, CrossGeom g, BwdPlan p, int* status) {
     using C = Cfg<D>;
-    constexpr int kRing = C::kRing;
+    constexpr int kRing = C::kRing, NB = C::kBufs, kShare = C::kShare;
     constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
@@ -145,7 +150,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         ptx::mbar_init_fence();
     }
     if (warp == 0) {
-        ptx::tmem_alloc(&sb->tmem, 512);
+        ptx::tmem_alloc(&sb->tmem, C::kCols);
         ptx::tmem_relinquish();
         ptx::tc_fence_before();
     }
@@ -168,12 +173,12 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                 ok = wait_or_abort(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status);
                 const uint64_t r1 = k_major<D>(row_tile(use)), r2 = k_major<D>(row_tile(use) + C::kRow);
                 for (int b = 0; ok && b < x.nb; ++b, ++i) {
-                    const int stage = i % kRing, buf = i & 1;
+                    const int stage = i % kRing, buf = i % NB;
                     const uint32_t cols = tmem + (uint32_t)buf * 128u;
                     const uint64_t c1 = k_major<D>(col_tile(stage)), c2 = k_major<D>(col_tile(stage) + C::kCol);
                     // the buffer holds the P and dS of two blocks ago until their products end
                     if (!wait_or_abort(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status) ||
-                        (i >= 2 && !wait_or_abort(&sb->acc_done[buf], ((i >> 1) - 1) & 1, &sb->abort, status))) {
+                        (i >= NB && !wait_or_abort(&sb->acc_done[buf], (i / NB - 1) & 1, &sb->abort, status))) {
                         ok = false;
                         break;
                     }
@@ -202,11 +207,11 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
                 const Unit x = unit_at<STATES>(g, p, u);
                 for (int b = 0; b < x.nb; ++b, ++i) {
-                    const int stage = i % kRing, buf = i & 1;
+                    const int stage = i % kRing, buf = i % NB;
                     const uint64_t c1 = n_major<D>(col_tile(stage), BN);
                     const uint64_t c2 = STATES ? n_major<D>(col_tile(stage) + C::kCol, BN) : c1;
                     const uint32_t cols = tmem + (uint32_t)buf * 128u;
-                    if (!wait_or_abort(&sb->p_full[buf], (i >> 1) & 1, &sb->abort, status)) {
+                    if (!wait_or_abort(&sb->p_full[buf], (i / NB) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
@@ -342,7 +347,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         }
     } else {
         // ---------------------------------------------------- P, dS and the epilogue
-        const int part = (warp - kCtrl) >> 2, qd = warp & 3;  // columns 16 part .. + 15
+        const int part = (warp - kCtrl) >> 2, qd = warp & 3;  // 16-column parts ``part``, + kShare ..
         const int row = 32 * qd + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16);
         const float c2 = g.scale * kLog2e;
@@ -379,19 +384,21 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             }
             uint64_t rest2 = 0ull;
             for (int b = 0; b < x.nb; ++b, ++i) {
-                const int stage = i % kRing, buf = i & 1;
+                const int stage = i % kRing, buf = i % NB;
                 const uint32_t cols = lanes + (uint32_t)buf * 128u;
-                if (!warp_wait(&sb->s_full[buf], (i >> 1) & 1, &sb->abort, status) ||
+                if (!warp_wait(&sb->s_full[buf], (i / NB) & 1, &sb->abort, status) ||
                     !warp_wait(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN + part * 16;
-                if (STATES || block_cols<STATES>(x, b) > part * 16) {
+#pragma unroll
+                for (int pt = part; pt < kParts; pt += kShare) {
+                    if (!STATES && block_cols<STATES>(x, b) <= pt * 16) break;
+                    const float* stat = reinterpret_cast<const float*>(smem + C::kOffStat) + stage * 2 * BN + pt * 16;
                     uint32_t s[16], dp[16];
-                    ptx::tmem_load_pair(cols + part * 16, cols + C::kDp + part * 16, s, dp);
-                    const uint32_t w = STATES ? 0xffffu : (sb->words[stage][part >> 1] >> ((part & 1) * 16)) & 0xffffu;
+                    ptx::tmem_load_pair(cols + pt * 16, cols + C::kDp + pt * 16, s, dp);
+                    const uint32_t w = STATES ? 0xffffu : (sb->words[stage][pt >> 1] >> ((pt & 1) * 16)) & 0xffffu;
                     uint32_t pp[8], pd[8];
                     auto form = [&](bool masked) {
                         const uint64_t noff2 = ptx::pack_f32x2(noff, noff), nd2 = ptx::pack_f32x2(nd, nd);
@@ -429,8 +436,8 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     if (STATES || w == 0xffffu) form(false);
                     else form(true);
                     // over the first 8 of the 16 scores that this thread has read
-                    ptx::tmem_st8(cols + part * 16, pp);
-                    ptx::tmem_st8(cols + C::kDp + part * 16, pd);
+                    ptx::tmem_st8(cols + pt * 16, pp);
+                    ptx::tmem_st8(cols + C::kDp + pt * 16, pd);
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
@@ -438,7 +445,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->acc_done[(i - 1) & 1], ((i - 1) >> 1) & 1, &sb->abort, status)) break;
+                if (!warp_wait(&sb->acc_done[(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) break;
                 ptx::tc_fence_after();
             }
             bool live = x.nb > 0;
@@ -504,7 +511,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
     allow_dependents();
     if (warp == 0) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(tmem, C::kCols);
     }
 }
 
@@ -544,10 +551,9 @@ bra_status launch(const CrossGeom& g, int splits, const void* q, const void* k, 
     const int sms = sm_count();
     if (sms <= 0) return BRA_ERR_CUDA;
     auto* kernel = bra_cross_tc_backward_kernel<D, STATES>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
-        return BRA_ERR_CUDA;
-    const int grid = units < sms ? (int)units : sms;
-    const cudaError_t e = launch_after_previous(kernel, dim3(grid), dim3(kThreads), C::kSmem, stream, tr1, tr2, tc1,
+    if (!allow_shared<bra_cross_tc_backward_kernel<D, STATES>>(C::kSmem)) return BRA_ERR_CUDA;
+    const int most = sms * C::kCtas, grid = units < most ? (int)units : most;
+    const cudaError_t e = launch_after_previous(kernel, dim3(grid), dim3(C::kThreads), C::kSmem, stream, tr1, tr2, tc1,
                                                 tc2, (const T*)q, (const T*)k, (const T*)v, (const T*)o, lse,
                                                 (const T*)go, (T*)out1, (T*)out2, delta, parts, g, p, status);
     return e == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
@@ -567,12 +573,12 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 
 bool cross_tc_backward_covers(const CrossGeom& g) { return g.rows >= 128 && g.Lk >= 64; }
 
-// Enough row splits for the tiles of states to reach every SM, each of at least eight blocks of rows.
+// Enough row splits for the tiles of states to fill the SMs, each of at least eight blocks of rows.
 int cross_tc_backward_splits(const CrossGeom& g) {
-    const int sms = sm_count();
+    const int slots = sm_count() * (g.d == 32 ? Cfg<32>::kCtas : 1);
     const long long units = (long long)((g.Lk + 127) / 128) * g.kv_heads * g.B;
-    if (sms <= 0 || units <= 0 || units >= sms) return 1;
-    long long s = sms / units;
+    if (slots <= 0 || units <= 0 || units >= slots) return 1;
+    long long s = slots / units;
     const long long most = ((g.rows + BN - 1) / BN) / 8;
     if (s > most) s = most;
     return s < 1 ? 1 : (int)s;

@@ -589,8 +589,7 @@ bra_status launch_forward(const CrossGeom& g, int splits, const void* q, const v
                           float* lse, CrossParts parts, cudaStream_t stream) {
     using S = Fwd<D, WM, WN>;
     auto* kernel = bra_cross_tf32_kernel<D, WM, WN>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes) != cudaSuccess)
-        return BRA_ERR_CUDA;
+    if (!allow_shared<bra_cross_tf32_kernel<D, WM, WN>>(S::kBytes)) return BRA_ERR_CUDA;
     const int row_tiles = (g.rows + S::kRows - 1) / S::kRows;
     const long long grid = (long long)row_tiles * splits * g.kv_heads * g.B;
     if (grid > 0x7fffffffLL) return BRA_ERR_UNSUPPORTED;
@@ -613,10 +612,7 @@ bra_status backward_d(const CrossGeom& g, int splits, const void* q, const void*
                       const float* lse, const void* go, void* dq, void* dk, void* dv, float* delta, float* parts,
                       cudaStream_t stream) {
     using T = float;
-    if (cudaFuncSetAttribute(bra_cross_tf32_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)dq_smem<D>()) != cudaSuccess ||
-        cudaFuncSetAttribute(bra_cross_tf32_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)dkv_smem<D>()) != cudaSuccess)
+    if (!allow_shared<bra_cross_tf32_dq_kernel<D>>(dq_smem<D>()) || !allow_shared<bra_cross_tf32_dkv_kernel<D>>(dkv_smem<D>()))
         return BRA_ERR_CUDA;
     const int row_tiles = (g.rows + 63) / 64, key_tiles = (g.Lk + 63) / 64;
     const long long grid_q = (long long)row_tiles * g.kv_heads * g.B;

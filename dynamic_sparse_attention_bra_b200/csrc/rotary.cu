@@ -1,16 +1,18 @@
 // Rotary positions with several axes (time, height, width) on Q and K.
 // Pair i of a token turns by the angle pos[axis(i)] inv_freq[i]:
 //   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
-// the same for every head, so a CTA forms the sines and cosines of its tokens
-// once, in shared memory, and applies them to all heads of Q and K.
+// the same for every head, so a thread forms the sines and cosines of a few
+// pairs of a token, keeps them in registers and turns those pairs of all heads
+// of Q and K.
 //
-// Angles of far positions do not fit fp32 (a position of 100000 leaves 2^-7
-// of a turn), so position x frequency and its reduction to a fraction of a
-// turn are done in fp64; sine and cosine of the reduced angle in fp32.
+// Angles of far positions do not fit fp32 (a position of 100000 leaves 2^-7 of a
+// turn).  A frequency in turns is kept as a 64-bit fraction F; position x F modulo
+// 2^64 is then the angle modulo a turn, whole turns wrapping away, at the cost of
+// two integer multiply-adds and good to 2^-32 of a turn over all 32-bit positions.
+// Sine and cosine of the reduced angle are fp32.
 //
-// Bound by HBM: Q and K are read and written once, in 16-byte vectors, four
-// units a thread, whose loads are issued before the CTA's angles are formed, so
-// that forming them runs under the loads (ROTARY_NOTE).
+// Bound by HBM (Q and K are read and written once, in 16-byte vectors) and, with
+// few heads to share an angle, by the sines: ROTARY_NOTE
 #include "kernels.h"
 #include "rotary.h"
 #include "tma_host.h"
@@ -19,9 +21,8 @@ namespace bra {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxAngles = 2048;  // (token, pair) angles of a CTA: 16 KB of shared memory
-constexpr int kUnits = 4;         // units of a thread
-constexpr int kMaxTokens = 256;   // of a CTA
+constexpr int kMaxPairs = 256;
+constexpr int kHeads = 4;         // heads of a thread in flight
 
 // x / d for x d < 2^32, by the multiplier floor(2^32 / d) + 1 (d > 1): a CTA's
 // counts are small, and a division by a value known at launch would cost more
@@ -69,111 +70,111 @@ __device__ __forceinline__ typename Vec<T, V>::type narrow(const float (&f)[V]) 
     }
 }
 
+// A frequency (radians a position) as a fraction of a turn, times 2^64.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    // 1 / (2 pi) in two parts; f has 24 bits, so that f hi + the fma's rest is exact
+    const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+    const double t = (double)f * hi, rest = fma((double)f, hi, -t) + (double)f * lo;
+    const double frac = t - floor(t);  // exact
+    return (uint64_t)(frac * 18446744073709551616.0) + (uint64_t)(int64_t)(rest * 18446744073709551616.0);
+}
+
 // PAIRED: a unit is two vectors (split halves); else one (interleaved).
 template <typename T, int V, bool PAIRED>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_freq, T* qo, T* ko, RotaryGeom g,
-                  int tokens_per_cta, int units_turn, Divisor per_token, Divisor per_head, Divisor pairs) {
+                  int tokens_per_cta, int units_turn, Divisor units) {
     using U = typename Vec<T, V>::type;
-    __shared__ float2 table[kMaxAngles];
-    __shared__ int place[kMaxTokens][3];
+    constexpr int A = PAIRED ? V : (V > 1 ? V / 2 : 1);  // pairs of a unit
+    __shared__ uint64_t turns[kMaxPairs];
     // CTA = consecutive tokens of one entry
     const int b = blockIdx.y, l0 = blockIdx.x * tokens_per_cta, here = min(tokens_per_cta, g.L - l0);
-    const int units = here * (int)per_token.d;
     grid_dependency_wait();
+    for (int i = threadIdx.x; i < g.P; i += kThreads) {
+        const uint64_t f = turns_of(__ldcg(inv_freq + i));
+        turns[i] = g.inverse ? 0ull - f : f;
+    }
+    __syncthreads();
 
-    // the unit's channels c (and P + c), where they come from and go to
-    struct Unit {
-        const T* src;
-        T* dst;
-        int tab, c;  // first angle of the token; first channel, or -1
-        bool turn;
-        U a, z;
-    } un[kUnits];
-    auto fetch = [&](int u0) {
+    for (int item = threadIdx.x; item < here * (int)units.d; item += kThreads) {
+        const int tk = here > 1 ? divide(item, units) : 0, x = item - tk * (int)units.d, l = l0 + tk;
+        const bool turn = x < units_turn;
+        const int c = PAIRED && !turn ? 2 * g.P + (x - units_turn) * V : x * V;
+        const bool pair = PAIRED && turn;
+        const T* src[2] = {q + (size_t)b * g.q_batch + (size_t)l * g.q_row + c,
+                           k + (size_t)b * g.k_batch + (size_t)l * g.k_row + c};
+        T* dst[2] = {qo + (size_t)b * g.qo_batch + (size_t)l * g.qo_row + c,
+                     ko + (size_t)b * g.ko_batch + (size_t)l * g.ko_row + c};
+        U va[kHeads], vz[kHeads];
+        // heads h .. h + kHeads - 1 of Q and then K
+        auto fetch = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int u = u0 + i * kThreads;
-            un[i].c = -1;
-            if (u >= units) continue;
-            const int tk = here > 1 ? divide(u, per_token) : 0, w = u - tk * (int)per_token.d;
-            const int head = divide(w, per_head), x = w - head * (int)per_head.d, l = l0 + tk;
-            if (head < g.heads) {
-                un[i].src = q + (size_t)b * g.q_batch + (size_t)l * g.q_row + (size_t)head * g.d;
-                un[i].dst = qo + (size_t)b * g.qo_batch + (size_t)l * g.qo_row + (size_t)head * g.d;
-            } else {
-                un[i].src = k + (size_t)b * g.k_batch + (size_t)l * g.k_row + (size_t)(head - g.heads) * g.d;
-                un[i].dst = ko + (size_t)b * g.ko_batch + (size_t)l * g.ko_row + (size_t)(head - g.heads) * g.d;
+            for (int i = 0; i < kHeads; ++i) {
+                const int y = h + i;
+                if (y >= g.heads + g.kv_heads) break;
+                const T* s = y < g.heads ? src[0] + y * g.d : src[1] + (y - g.heads) * g.d;
+                va[i] = *reinterpret_cast<const U*>(s);
+                if (pair) vz[i] = *reinterpret_cast<const U*>(s + g.P);
             }
-            un[i].tab = tk * g.P;
-            un[i].turn = x < units_turn;
-            un[i].c = PAIRED && !un[i].turn ? 2 * g.P + (x - units_turn) * V : x * V;
-            un[i].a = *reinterpret_cast<const U*>(un[i].src + un[i].c);
-            if (PAIRED && un[i].turn) un[i].z = *reinterpret_cast<const U*>(un[i].src + g.P + un[i].c);
-        }
-    };
-    fetch(threadIdx.x);
-
-    for (int tk = threadIdx.x; tk < here; tk += kThreads) {
-        const int l = l0 + tk;
-        if (pos) {
-#pragma unroll
-            for (int axis = 0; axis < 3; ++axis)
-                place[tk][axis] = __ldcg(pos + (size_t)b * g.pos_batch + (size_t)l * 3 + axis);
-        } else {
-            const int row = l / g.W, t = row / g.H;
-            place[tk][0] = t;
-            place[tk][1] = row - t * g.H;
-            place[tk][2] = l - row * g.W;
-        }
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < here * g.P; e += kThreads) {
-        const int tk = divide(e, pairs), i = e - tk * g.P;
-        const int p = place[tk][i < g.axis1 ? 0 : (i < g.axis2 ? 1 : 2)];
-        // turns, reduced to [-1/2, 1/2]
-        double turns = (double)p * (double)__ldcg(inv_freq + i) * 0.15915494309189533577;
-        turns -= rint(turns);
-        float s, c;
-        sincospif(2.f * (float)turns, &s, &c);
-        table[e] = make_float2(c, g.inverse ? -s : s);
-    }
-    __syncthreads();
-
-    for (int u0 = threadIdx.x; u0 < units; u0 += kUnits * kThreads) {
-        if (u0 != (int)threadIdx.x) fetch(u0);
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int c = un[i].c;
-            if (c < 0) continue;
-            const float2* tab = table + un[i].tab;
-            if (!un[i].turn) {
-                *reinterpret_cast<U*>(un[i].dst + c) = un[i].a;
-            } else if constexpr (PAIRED) {
-                float f[V], h[V];
-                widen<T, V>(un[i].a, f);
-                widen<T, V>(un[i].z, h);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float2 t = tab[c + e];
-                    const float y = f[e] * t.x - h[e] * t.y;
-                    h[e] = h[e] * t.x + f[e] * t.y;
-                    f[e] = y;
-                }
-                *reinterpret_cast<U*>(un[i].dst + c) = narrow<T, V>(f);
-                *reinterpret_cast<U*>(un[i].dst + g.P + c) = narrow<T, V>(h);
+        };
+        fetch(0);
+        float cs[A], sn[A];
+        if (turn) {
+            int p0, p1, p2;
+            if (pos) {
+                const int32_t* at = pos + (size_t)b * g.pos_batch + (size_t)l * 3;
+                p0 = __ldcg(at);
+                p1 = __ldcg(at + 1);
+                p2 = __ldcg(at + 2);
             } else {
-                float f[V];
-                widen<T, V>(un[i].a, f);
+                const int row = l / g.W;
+                p0 = row / g.H;
+                p1 = row - p0 * g.H;
+                p2 = l - row * g.W;
+            }
 #pragma unroll
-                for (int e = 0; e < V; e += 2) {
-                    if ((c + e) / 2 >= g.P) continue;  // the last unit may hold channels past the pairs
-                    const float2 t = tab[(c + e) / 2];
-                    const float y = f[e] * t.x - f[e + 1] * t.y;
-                    f[e + 1] = f[e + 1] * t.x + f[e] * t.y;
-                    f[e] = y;
+            for (int e = 0; e < A; ++e) {
+                const int i = PAIRED ? c + e : c / 2 + e;
+                if (i >= g.P) break;  // (interleaved: the last unit may hold channels past the pairs)
+                const int p = i < g.axis1 ? p0 : (i < g.axis2 ? p1 : p2);
+                // the product's upper half, a signed fraction of a turn
+                const int angle = (int)(((uint64_t)(int64_t)p * turns[i]) >> 32);
+                sincospif((float)angle * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
+            }
+        }
+        for (int h = 0; h < g.heads + g.kv_heads; h += kHeads) {
+            if (h > 0) fetch(h);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int y = h + i;
+                if (y >= g.heads + g.kv_heads) break;
+                T* d = y < g.heads ? dst[0] + y * g.d : dst[1] + (y - g.heads) * g.d;
+                if (!turn) {
+                    *reinterpret_cast<U*>(d) = va[i];
+                } else if constexpr (PAIRED) {
+                    float f[V], z[V];
+                    widen<T, V>(va[i], f);
+                    widen<T, V>(vz[i], z);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float w = f[e] * cs[e] - z[e] * sn[e];
+                        z[e] = z[e] * cs[e] + f[e] * sn[e];
+                        f[e] = w;
+                    }
+                    *reinterpret_cast<U*>(d) = narrow<T, V>(f);
+                    *reinterpret_cast<U*>(d + g.P) = narrow<T, V>(z);
+                } else {
+                    float f[V];
+                    widen<T, V>(va[i], f);
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        if ((c + e) / 2 >= g.P) break;
+                        const float w = f[e] * cs[e / 2] - f[e + 1] * sn[e / 2];
+                        f[e + 1] = f[e + 1] * cs[e / 2] + f[e] * sn[e / 2];
+                        f[e] = w;
+                    }
+                    *reinterpret_cast<U*>(d) = narrow<T, V>(f);
                 }
-                *reinterpret_cast<U*>(un[i].dst + c) = narrow<T, V>(f);
             }
         }
     }
@@ -184,22 +185,18 @@ template <typename T, int V, bool PAIRED>
 cudaError_t launch(const RotaryGeom& g, const void* q, const void* k, const int32_t* pos, const float* inv_freq,
                    void* q_out, void* k_out, cudaStream_t stream) {
     const int units_turn = PAIRED ? g.P / V : (2 * g.P + V - 1) / V;
-    const int units_head = PAIRED ? units_turn + (g.d - 2 * g.P) / V : g.d / V;
-    const int units_token = (g.heads + g.kv_heads) * units_head;
-    // tokens of a CTA: kUnits units a thread, in at least two CTAs for each SM
+    const int units = PAIRED ? units_turn + (g.d - 2 * g.P) / V : g.d / V;
+    // a unit a thread and pass; two passes where that still gives each SM four CTAs
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const long long spread = (long long)g.B * g.L / (2LL * sms) + 1;
-    int per = kUnits * kThreads / units_token;
-    if (per > kMaxAngles / g.P) per = kMaxAngles / g.P;
-    if (per > kMaxTokens) per = kMaxTokens;
+    const long long items = (long long)g.B * g.L * units;
+    int per = (items > 8LL * kThreads * sms ? 2 : 1) * kThreads / units;
     if (per > g.L) per = g.L;
-    if (per > spread) per = (int)spread;
     if (per < 1) per = 1;
     return launch_after_previous(bra_rotary_kernel<T, V, PAIRED>, dim3((unsigned)((g.L + per - 1) / per), (unsigned)g.B),
                                  dim3(kThreads), 0, stream, static_cast<const T*>(q), static_cast<const T*>(k), pos,
                                  inv_freq, static_cast<T*>(q_out), static_cast<T*>(k_out), g, per, units_turn,
-                                 divisor(units_token), divisor(units_head), divisor(g.P));
+                                 divisor(units));
 }
 
 }  // namespace

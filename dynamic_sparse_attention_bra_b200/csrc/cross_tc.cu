@@ -113,7 +113,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = ptx::smem_addr(smem);
     Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kOffBar);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
@@ -147,7 +147,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 
     if (warp < 2) {
         // ------------------------------------------------ products of tile ``warp``
-        if (lane == 0) {
+        {
             const int grp = warp;
             const uint32_t cols = tmem + (uint32_t)grp * C::kGroupCols;
             const uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
@@ -156,9 +156,9 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             // S = Q K^T of block ``at`` (the tile's b-th)
             auto qk = [&](const Unit& x, int b, int at) -> bool {
                 const int stage = at % kRing, buf = at % NB;
-                if (!wait_or_abort(&sb->kv_full[stage], (at / kRing) & 1, &sb->abort, status)) return false;
+                if (!warp_wait(&sb->kv_full[stage], (at / kRing) & 1, &sb->abort, status)) return false;
                 // the buffer's last S: read, or (P shares its columns) used by its P V
-                if (at >= NB && !wait_or_abort(C::kAlias ? &sb->o_done[grp][buf] : &sb->s_free[grp][buf],
+                if (at >= NB && !warp_wait(C::kAlias ? &sb->o_done[grp][buf] : &sb->s_free[grp][buf],
                                                (at / NB - 1) & 1, &sb->abort, status))
                     return false;
                 ptx::tc_fence_after();
@@ -167,15 +167,15 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<BN>(x.n, x.t0 + b), false, false);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_bf16(cols + (uint32_t)buf * 64u, qd + k_step<D>(kk, 128), kd + k_step<D>(kk, BN), idesc, kk);
-                ptx::mma_commit(&sb->s_full[grp][buf]);
-                if (b == x.nb - 1) ptx::mma_commit(&sb->q_empty[grp][use & 1]);
+                    ptx::warp_mma_bf16(cols + (uint32_t)buf * 64u, qd + k_step<D>(kk, 128), kd + k_step<D>(kk, BN), idesc, kk);
+                ptx::warp_mma_commit(&sb->s_full[grp][buf]);
+                if (b == x.nb - 1) ptx::warp_mma_commit(&sb->q_empty[grp][use & 1]);
                 return true;
             };
             // O += P V
             auto pv = [&](const Unit& x, int b, int at) -> bool {
                 const int stage = at % kRing, buf = at % NB;
-                if (!wait_or_abort(&sb->p_full[grp][buf], (at / NB) & 1, &sb->abort, status)) return false;
+                if (!warp_wait(&sb->p_full[grp][buf], (at / NB) & 1, &sb->abort, status)) return false;
                 ptx::tc_fence_after();
                 const uint64_t vd = n_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile, BN);
                 const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
@@ -183,21 +183,21 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                     if (kk < steps)
-                        ptx::mma_bf16_ta(cols + C::kO, pt + (uint32_t)kk * 8u, vd + n_step<D>(kk), idesc_o,
+                        ptx::warp_mma_bf16_ta(cols + C::kO, pt + (uint32_t)kk * 8u, vd + n_step<D>(kk), idesc_o,
                                          kk > 0 ? 1u : (uint32_t)(b > 0));
-                ptx::mma_commit(&sb->o_done[grp][buf]);
-                ptx::mma_commit(&sb->kv_empty[stage]);
+                ptx::warp_mma_commit(&sb->o_done[grp][buf]);
+                ptx::warp_mma_commit(&sb->kv_empty[stage]);
                 return true;
             };
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
                 const Unit x = unit_at<BN>(g, p, u);
                 if (x.nb == 0) continue;
-                ok = wait_or_abort(&sb->q_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status) && qk(x, 0, i);
+                ok = warp_wait(&sb->q_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status) && qk(x, 0, i);
                 for (int b = 0; ok && b < x.nb; ++b) ok = (b + 1 == x.nb || qk(x, b + 1, i + b + 1)) && pv(x, b, i + b);
                 i += x.nb;
                 ++use;
             }
-            ptx::mma_commit(&sb->drain[grp]);
+            ptx::warp_mma_commit(&sb->drain[grp]);
             ptx::mbar_wait(&sb->drain[grp], 0, kWait);
         }
         __syncwarp();

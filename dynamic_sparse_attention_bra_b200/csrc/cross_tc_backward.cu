@@ -15,12 +15,14 @@
 // S and dP have two buffers (256 columns; the sums take 2 d of the others), so
 // that the products of the next block run under the exponentials of this one (d =
 // 32: one buffer, and two CTAs on an SM, which also hide the ends of short units).
-// There is no maximum to agree on, so four (two) threads share a row, in parts of
-// 16 columns.  Roles of the warps: 0 issues S and dP, 1 the sums' products; 2 starts the
-// loads (TMA, or cp.async where no map can be made); 3 passes each landed tile
-// on, after it has zeroed the rows of masked or missing states (what is stored
-// there must not reach a product) and, for dK and dV, added the columns' log sums
-// and D; from 4 on, four warps for each share of the columns, the rows' threads.
+// There is no maximum to agree on, so two threads share a row, in parts of 16
+// columns, and (d >= 64) two groups of such threads take the blocks in turn: a
+// block's waits and TMEM latencies cost its threads as much as its arithmetic.
+// Roles of the warps: 0 issues S and dP, 1 the sums' products; 2 starts the loads
+// (TMA, or cp.async where no map can be made); 3 passes each landed tile on, after
+// it has zeroed the rows of masked or missing states (what is stored there must
+// not reach a product) and, for dK and dV, added the columns' log sums and D; from
+// 4 on the rows' threads.
 // With two tiles of 128 rows a CTA, one buffer, and a thread a row (the first
 // form) a block's products and exponentials took turns: 4250 clocks for two
 // tiles, of which a row's threads waited 2360.
@@ -43,8 +45,8 @@ constexpr int BN = 64;      // columns of a block
 struct Barriers {
     uint64_t c_land[kStages], c_full[kStages], c_empty[kStages];
     uint64_t r_land[2], r_full[2], r_empty[2];
-    uint64_t s_full[2], p_full[2], acc_done[2];  // [buffer]
-    uint64_t rest_full, drain[2];
+    uint64_t s_full[3], p_full[3], acc_done[3];  // [buffer]
+    uint64_t rest_full, epi_done, drain[2];
     uint32_t words[kStages][2];  // dQ: the block's valid states
     uint32_t row_words[2][4];    // dK, dV: the tile's
     uint32_t tmem;
@@ -54,9 +56,11 @@ struct Barriers {
 template <int D>
 struct Cfg {
     static constexpr int kCtas = D == 32 ? 2 : 1;   // on an SM
-    static constexpr int kBufs = D == 32 ? 1 : 2;   // of S and dP
-    static constexpr int kShare = D == 32 ? 2 : 4;  // threads of a row
-    static constexpr int kThreads = 32 * (kCtrl + 4 * kShare);
+    static constexpr int kBufs = D == 32 ? 1 : D == 64 ? 3 : 2;  // of S and dP
+    static constexpr int kGroups = D == 32 ? 1 : 2;  // of row threads, taking blocks in turn
+    static constexpr int kShare = 2;                 // threads of a row in a group
+    static constexpr int kRowThreads = 128 * kGroups * kShare;
+    static constexpr int kThreads = 32 * kCtrl + kRowThreads;
     // TMEM: buffer x: S at 128 x, dP at 128 x + 64 (P and dS over them); sums
     static constexpr uint32_t kCols = D == 32 ? 256 : 512;
     static constexpr uint32_t kDp = 64, kAcc1 = 128 * kBufs, kAcc2 = 128 * kBufs + D;
@@ -65,7 +69,7 @@ struct Cfg {
     // rows [buffer] x (R1 | R2), then stages of C1 | C2, the columns' statistics (dQ: a row's sums of dS), barriers
     static constexpr uint32_t kOffCol = 2 * 2 * kRow;
     static constexpr uint32_t kOffStat = kOffCol + kRing * 2 * kCol;
-    static constexpr uint32_t kStat = kRing * 2 * BN * 4 > 128 * kShare * 4 ? kRing * 2 * BN * 4 : 128 * kShare * 4;
+    static constexpr uint32_t kStat = kRing * 2 * BN * 4 > kRowThreads * 4 ? kRing * 2 * BN * 4 : kRowThreads * 4;
     static constexpr uint32_t kOffBar = kOffStat + kStat;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers);  // (no room for an alignment's slack)
     static_assert(kSmem <= 227u * 1024u, "shared memory");
@@ -119,7 +123,8 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                              const __nv_bfloat16* o, const float* lse, const __nv_bfloat16* go, __nv_bfloat16* out1,
                              __nv_bfloat16* out2, float* delta, float* parts, CrossGeom g, BwdPlan p, int* status) {
     using C = Cfg<D>;
-    constexpr int kRing = C::kRing, NB = C::kBufs, kShare = C::kShare;
+    constexpr int kRing = C::kRing, NB = C::kBufs, kShare = C::kShare, kGroups = C::kGroups;
+    constexpr int kEach = kShare * kGroups;  // threads of a row
     constexpr int kPanels = D == 128 ? 2 : 1;  // of 64 channels (D = 32: one of 32)
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
@@ -128,7 +133,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         return;
     }
     Barriers* sb = reinterpret_cast<Barriers*>(smem + C::kOffBar);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
@@ -139,13 +144,16 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(&sb->r_land[x], 1);
             ptx::mbar_init(&sb->r_full[x], 1);
-            ptx::mbar_init(&sb->r_empty[x], STATES ? 1 : 1 + 128 * kShare);  // the products; the reads of dO for D
+            ptx::mbar_init(&sb->r_empty[x], STATES ? 1 : 1 + C::kRowThreads);  // the products; the reads of dO for D
+            ptx::mbar_init(&sb->drain[x], 1);
+        }
+        for (int x = 0; x < NB; ++x) {
             ptx::mbar_init(&sb->s_full[x], 1);
             ptx::mbar_init(&sb->p_full[x], 128 * kShare);
             ptx::mbar_init(&sb->acc_done[x], 1);
-            ptx::mbar_init(&sb->drain[x], 1);
         }
-        ptx::mbar_init(&sb->rest_full, 128 * kShare);
+        ptx::mbar_init(&sb->rest_full, C::kRowThreads);
+        ptx::mbar_init(&sb->epi_done, C::kRowThreads);
         sb->abort = 0;
         ptx::mbar_init_fence();
     }
@@ -164,21 +172,21 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
 
     if (warp == 0) {
         // -------------------------------------------------------------- S and dP
-        if (lane == 0) {
+        {
             int i = 0, use = 0;  // blocks and units so far
             bool ok = true;
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
                 const Unit x = unit_at<STATES>(g, p, u);
                 if (x.nb == 0) continue;
-                ok = wait_or_abort(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status);
+                ok = warp_wait(&sb->r_full[use & 1], (use >> 1) & 1, &sb->abort, status);
                 const uint64_t r1 = k_major<D>(row_tile(use)), r2 = k_major<D>(row_tile(use) + C::kRow);
                 for (int b = 0; ok && b < x.nb; ++b, ++i) {
                     const int stage = i % kRing, buf = i % NB;
                     const uint32_t cols = tmem + (uint32_t)buf * 128u;
                     const uint64_t c1 = k_major<D>(col_tile(stage)), c2 = k_major<D>(col_tile(stage) + C::kCol);
                     // the buffer holds the P and dS of two blocks ago until their products end
-                    if (!wait_or_abort(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status) ||
-                        (i >= NB && !wait_or_abort(&sb->acc_done[buf], (i / NB - 1) & 1, &sb->abort, status))) {
+                    if (!warp_wait(&sb->c_full[stage], (i / kRing) & 1, &sb->abort, status) ||
+                        (i >= NB && !warp_wait(&sb->acc_done[buf], (i / NB - 1) & 1, &sb->abort, status))) {
                         ok = false;
                         break;
                     }
@@ -186,32 +194,34 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<STATES>(x, b), false, false);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        ptx::mma_bf16(cols, r1 + k_step<D>(kk, 128), c1 + k_step<D>(kk, BN), idesc, kk);
-                        ptx::mma_bf16(cols + C::kDp, r2 + k_step<D>(kk, 128), c2 + k_step<D>(kk, BN), idesc, kk);
+                        ptx::warp_mma_bf16(cols, r1 + k_step<D>(kk, 128), c1 + k_step<D>(kk, BN), idesc, kk);
+                        ptx::warp_mma_bf16(cols + C::kDp, r2 + k_step<D>(kk, 128), c2 + k_step<D>(kk, BN), idesc, kk);
                     }
-                    ptx::mma_commit(&sb->s_full[buf]);
-                    if (b == x.nb - 1) ptx::mma_commit(&sb->r_empty[use & 1]);
+                    ptx::warp_mma_commit(&sb->s_full[buf]);
+                    if (b == x.nb - 1) ptx::warp_mma_commit(&sb->r_empty[use & 1]);
                 }
                 ++use;
             }
-            ptx::mma_commit(&sb->drain[0]);
+            ptx::warp_mma_commit(&sb->drain[0]);
             ptx::mbar_wait(&sb->drain[0], 0, kWait);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------- the sums
-        if (lane == 0) {
+        {
             const uint32_t idesc = ptx::idesc_bf16_f32(128, D, false, true);
-            int i = 0;
+            int i = 0, use = 0;
             bool ok = true;
             for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
                 const Unit x = unit_at<STATES>(g, p, u);
+                // the last unit's sums have been read
+                if (x.nb > 0 && use++ > 0 && !warp_wait(&sb->epi_done, (use - 2) & 1, &sb->abort, status)) break;
                 for (int b = 0; b < x.nb; ++b, ++i) {
                     const int stage = i % kRing, buf = i % NB;
                     const uint64_t c1 = n_major<D>(col_tile(stage), BN);
                     const uint64_t c2 = STATES ? n_major<D>(col_tile(stage) + C::kCol, BN) : c1;
                     const uint32_t cols = tmem + (uint32_t)buf * 128u;
-                    if (!wait_or_abort(&sb->p_full[buf], (i / NB) & 1, &sb->abort, status)) {
+                    if (!warp_wait(&sb->p_full[buf], (i / NB) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
@@ -221,14 +231,14 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     for (int kk = 0; kk < BN / 16; ++kk)
                         if (kk < steps) {
                             const uint32_t a = cols + (uint32_t)kk * 16u, more = kk > 0 ? 1u : (uint32_t)(b > 0);
-                            ptx::mma_bf16_ta(tmem + C::kAcc1, a + C::kDp, c1 + n_step<D>(kk), idesc, more);
-                            ptx::mma_bf16_ta(tmem + C::kAcc2, a, c2 + n_step<D>(kk), idesc, more);
+                            ptx::warp_mma_bf16_ta(tmem + C::kAcc1, a + C::kDp, c1 + n_step<D>(kk), idesc, more);
+                            ptx::warp_mma_bf16_ta(tmem + C::kAcc2, a, c2 + n_step<D>(kk), idesc, more);
                         }
-                    ptx::mma_commit(&sb->acc_done[buf]);
-                    ptx::mma_commit(&sb->c_empty[stage]);
+                    ptx::warp_mma_commit(&sb->acc_done[buf]);
+                    ptx::warp_mma_commit(&sb->c_empty[stage]);
                 }
             }
-            ptx::mma_commit(&sb->drain[1]);
+            ptx::warp_mma_commit(&sb->drain[1]);
             ptx::mbar_wait(&sb->drain[1], 0, kWait);
         }
         __syncwarp();
@@ -347,7 +357,8 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
         }
     } else {
         // ---------------------------------------------------- P, dS and the epilogue
-        const int part = (warp - kCtrl) >> 2, qd = warp & 3;  // 16-column parts ``part``, + kShare ..
+        // 16-column parts ``part``, + kShare .. of the group's blocks; ``mine`` of the row's threads
+        const int mine = (warp - kCtrl) >> 2, part = mine % kShare, grp = mine / kShare, qd = warp & 3;
         const int row = 32 * qd + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16);
         const float c2 = g.scale * kLog2e;
@@ -384,6 +395,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             }
             uint64_t rest2 = 0ull;
             for (int b = 0; b < x.nb; ++b, ++i) {
+                if (kGroups > 1 && i % kGroups != grp) continue;
                 const int stage = i % kRing, buf = i % NB;
                 const uint32_t cols = lanes + (uint32_t)buf * 128u;
                 if (!warp_wait(&sb->s_full[buf], (i / NB) & 1, &sb->abort, status) ||
@@ -459,20 +471,20 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     float lo, hi;
                     ptx::unpack_f32x2(rest2, lo, hi);
                     float* rests = reinterpret_cast<float*>(smem + C::kOffStat);
-                    rests[part * 128 + row] = lo + hi;
+                    rests[mine * 128 + row] = lo + hi;
                     ptx::mbar_arrive(&sb->rest_full);
                     if (!warp_wait(&sb->rest_full, use & 1, &sb->abort, status)) break;
 #pragma unroll
-                    for (int y = 0; y < kShare; ++y) rest += rests[y * 128 + row];
+                    for (int y = 0; y < kEach; ++y) rest += rests[y * 128 + row];
                 }
                 if (in) {
                     at = cross_o_offset(g, x.b, x.j, r0);
-                    if (part == 0) delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
+                    if (mine == 0) delta[cross_lse_offset(g, x.b, x.j, r0)] = rest - nd;
                 }
             }
             const size_t elems = (size_t)g.B * g.Lk * g.kv_heads * D;
 #pragma unroll 1
-            for (int c = part * (D / kShare); c < (part + 1) * (D / kShare); c += 8) {
+            for (int c = mine * (D / kEach); c < (mine + 1) * (D / kEach); c += 8) {
                 uint32_t a1[8], a2[8];
                 if (x.nb > 0) ptx::tmem_load_pair(lanes + C::kAcc1 + c, lanes + C::kAcc2 + c, a1, a2);
                 if (!in) continue;
@@ -501,8 +513,11 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                                        ptx::pack_bf16x2(f2[4], f2[5]), ptx::pack_bf16x2(f2[6], f2[7]));
                 }
             }
-            if (x.nb > 0) ++use;
-            ptx::tc_fence_before();  // the sums are read before the next tile's first products, which p_full orders after
+            if (x.nb > 0) {
+                ++use;
+                ptx::tc_fence_before();  // the next unit's first products may overwrite the sums
+                ptx::mbar_arrive(&sb->epi_done);
+            }
         }
     }
 

@@ -81,7 +81,7 @@ bra_status cross_forward_short(const CrossGeom& g, const void* q, const void* k,
                                cudaStream_t stream);
 // The form for many rows (tcgen05); covers() says from how many on it is taken.
 bool cross_tc_covers(const CrossGeom& g);
-int cross_tc_rows();
+int cross_tc_rows(const CrossGeom& g);
 bra_status cross_forward_tc(const CrossGeom& g, int splits, const void* q, const void* k, const void* v, void* o,
                             float* lse, CrossParts parts, int* status, cudaStream_t stream);
 bra_status cross_forward_f32(const CrossGeom& g, const CrossPlan& p, const void* q, const void* k, const void* v,

@@ -358,7 +358,7 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 
 int rows_per_cta(const CrossGeom& g, bool bf16) {
     if (!bf16) return g.rows <= 16 ? 16 : 64;
-    if (cross_tc_covers(g)) return cross_tc_rows();
+    if (cross_tc_covers(g)) return cross_tc_rows(g);
     return g.rows <= 16 ? 16 : (g.d == 32 ? 128 : 64);
 }
 

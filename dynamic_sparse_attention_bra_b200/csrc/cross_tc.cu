@@ -2,28 +2,27 @@
 // form for many rows (a map's tokens, a decoder's prompt).  The mathematics
 // is that of cross_mma.cu.
 //
-// A unit of work is 256 rows of one (entry, state head), two tiles of 128, and
-// a range of the states, streamed in blocks of 128 (64 at d = 128) that both tiles
-// share.  Per tile and block: S = Q K^T (M 128, N = the block) lands in TMEM; a softmax
-// thread per row takes its scores into registers, writes P as bf16 into TMEM,
-// and O += P V (P the TMEM operand, N = d) accumulates in TMEM.  O is rescaled only where a row's maximum has grown by more than 2^8
-// since the last rescale (until then P may exceed 1: its relative rounding
-// is the same, and l, in fp32, uses the same offset), so that the common
-// block costs no pass over O.
+// A unit of work is two tiles of 128 rows (four at d = 32) of one (entry, state
+// head) and a range of the states, streamed in blocks of 64 (128 at d = 64) that
+// its tiles share.  Per tile and block: S = Q K^T (M 128, N = the block) lands in
+// TMEM; a softmax thread per row takes its scores into registers, writes P as bf16
+// into TMEM, and O += P V (P the TMEM operand, N = d) accumulates in TMEM.  O is
+// rescaled only where a row's maximum has grown by more than 2^8 since the last
+// rescale (until then P may exceed 1: its relative rounding is the same, and l, in
+// fp32, uses the same offset), so that the common block costs no pass over O.
 //
-// Roles of the 12 warps, one CTA on an SM: 0, 1 issue the products of tile 0, 1;
-// 2 starts the loads of K and V, and of both tiles' Q (double-buffered), by TMA
+// Roles of the warps, one CTA on an SM: 0, 1 issue the products of the even, odd
+// tiles; 2 starts the loads of K and V, and of the tiles' Q (double-buffered), by TMA
 // (cp.async where no map can be made); 3 passes each landed block on, after it has
 // zeroed V's rows of masked or missing states, so that what is stored there never
-// reaches a product; 4-7, 8-11 are the tiles' softmax. For d <= 64 the next S is issued as
-// soon as the scores are in registers, under the exponentials.  For d = 128 the
-// columns do not suffice for a P of its own: P takes its S's, and S has two
-// buffers, so that the next S is there before this softmax ends.
+// reaches a product; from 4 on, four warps for each tile, the softmax.  For d <= 64
+// the next S is issued as soon as the scores are in registers, under the
+// exponentials.  For d = 128 the columns do not suffice for a P of its own: P
+// takes its S's, and S has two buffers, so that the next S is there before this
+// softmax ends.
 //
-// Blocks of 64 for d <= 64, with two CTAs of 96 registers a thread on an SM, and
-// with one CTA and two buffers of S and P, were slower (127 and 168 us where this
-// form takes HIGHRES, 16384 rows over 4096 states): a block's waits and the
-// latency of its score load cost about 900 clocks whatever its width.
+// d = 32: a block costs a tile's threads its waits and TMEM latencies besides the
+// exponentials, so four tiles' share an SM: TILES_NOTE
 //
 // Bound by the exponentials (16 a clock and SM) for d = 32, by them and the
 // products for d = 128.  Every mbarrier wait is bounded; on expiry the kernel
@@ -38,15 +37,14 @@ namespace {
 using namespace cross;
 
 constexpr int kCtrl = 4;
-constexpr int kThreads = 32 * (kCtrl + 8);
 constexpr int kStages = 4;  // at most
 constexpr float kGrow = 8.f;  // powers of two a maximum may grow by before O is rescaled
 
 struct Barriers {
     uint64_t kv_land[kStages], kv_full[kStages], kv_empty[kStages];
-    uint64_t q_full[2][2], q_empty[2][2];
+    uint64_t q_full[4][2], q_empty[4][2];
     // [tile][buffer of the block]
-    uint64_t s_full[2][2], s_free[2][2], p_full[2][2], o_done[2][2];
+    uint64_t s_full[4][2], s_free[4][2], p_full[4][2], o_done[4][2];
     uint64_t drain[2];
     uint32_t words[kStages][4];  // the block's valid states
     uint32_t tmem;
@@ -55,23 +53,25 @@ struct Barriers {
 
 template <int D>
 struct Cfg {
-    static constexpr int kBlock = D == 128 ? 64 : 128;  // states of a block
+    static constexpr int kTiles = D == 32 ? 4 : 2;      // of 128 rows in a unit
+    static constexpr int kThreads = 32 * (kCtrl + 4 * kTiles);
+    static constexpr int kBlock = D == 64 ? 128 : 64;   // states of a block
     static constexpr int kBufs = D == 128 ? 2 : 1;      // of S and P
     static constexpr bool kAlias = D == 128;            // P in its S's columns
     static constexpr uint32_t kCols = 512;
-    static constexpr uint32_t kGroupCols = 256;
+    static constexpr uint32_t kTileCols = kCols / kTiles;
     // buffer x: S at x * 64, P at kP + x * 64; O
-    static constexpr uint32_t kP = kAlias ? 0 : 128, kO = kAlias ? 128 : 192;
+    static constexpr uint32_t kP = kAlias ? 0 : kBlock, kO = kAlias ? 128 : kBlock + kBlock / 2;
     static constexpr uint32_t kQTile = 128u * D * 2u, kKvTile = (uint32_t)kBlock * D * 2u;
     static constexpr int kRing = D == 128 ? 3 : 4;  // stages that fit beside Q
-    static constexpr uint32_t kOffKv = 4 * kQTile;  // Q [group][2], then stages of K | V
+    static constexpr uint32_t kOffKv = 2 * kTiles * kQTile;  // Q [tile][2], then stages of K | V
     static constexpr uint32_t kOffBar = kOffKv + (uint32_t)kRing * 2u * kKvTile;
     static constexpr uint32_t kSmem = kOffBar + (uint32_t)sizeof(Barriers) + 1024u;
     static_assert(kSmem <= 227u * 1024u, "shared memory");
 };
 
 struct TcPlan {
-    int pairs;    // units of 256 rows in a (entry, state head)
+    int groups;   // units' rows in a (entry, state head)
     int splits;
     int units;
     int tma_q, tma_kv;  // loads by TMA (a map could be made)
@@ -81,11 +81,11 @@ struct Unit {
     int b, j, row0, split, n, t0, nb;  // first block and number of blocks
 };
 
-template <int BN>
+template <int BN, int ROWS>
 __device__ __forceinline__ Unit unit_at(const CrossGeom& g, const TcPlan& p, int u) {
     Unit x;
-    x.row0 = (u % p.pairs) * 256;
-    u /= p.pairs;
+    x.row0 = (u % p.groups) * ROWS;
+    u /= p.groups;
     x.split = u % p.splits;
     u /= p.splits;
     x.j = u % g.kv_heads;
@@ -102,7 +102,7 @@ template <int BN>
 __device__ __forceinline__ int block_cols(int n, int t) { return (min(BN, n - t * BN) + 15) & ~15; }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                     const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
@@ -119,9 +119,9 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         for (int i = 0; i < kRing; ++i) {
             ptx::mbar_init(&sb->kv_land[i], 1);
             ptx::mbar_init(&sb->kv_full[i], 1);
-            ptx::mbar_init(&sb->kv_empty[i], 2);
+            ptx::mbar_init(&sb->kv_empty[i], C::kTiles);
         }
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < C::kTiles; ++x) {
             for (int y = 0; y < 2; ++y) {
                 ptx::mbar_init(&sb->q_full[x][y], 1);
                 ptx::mbar_init(&sb->q_empty[x][y], 1);
@@ -130,7 +130,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 ptx::mbar_init(&sb->p_full[x][y], 128);
                 ptx::mbar_init(&sb->o_done[x][y], 1);
             }
-            ptx::mbar_init(&sb->drain[x], 1);
+            if (x < 2) ptx::mbar_init(&sb->drain[x], 1);
         }
         sb->abort = 0;
         ptx::mbar_init_fence();
@@ -146,60 +146,84 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     grid_dependency_wait();
 
     if (warp < 2) {
-        // ------------------------------------------------ products of tile ``warp``
-        {
-            const int grp = warp;
-            const uint32_t cols = tmem + (uint32_t)grp * C::kGroupCols;
-            const uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
-            int i = 0, use = 0;  // blocks and tiles so far
-            bool ok = true;
-            // S = Q K^T of block ``at`` (the tile's b-th)
-            auto qk = [&](const Unit& x, int b, int at) -> bool {
-                const int stage = at % kRing, buf = at % NB;
-                if (!warp_wait(&sb->kv_full[stage], (at / kRing) & 1, &sb->abort, status)) return false;
-                // the buffer's last S: read, or (P shares its columns) used by its P V
-                if (at >= NB && !warp_wait(C::kAlias ? &sb->o_done[grp][buf] : &sb->s_free[grp][buf],
-                                               (at / NB - 1) & 1, &sb->abort, status))
-                    return false;
-                ptx::tc_fence_after();
-                const uint64_t qd = k_major<D>(sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile);
-                const uint64_t kd = k_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile);
-                const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<BN>(x.n, x.t0 + b), false, false);
+        // ---------------------------------------- products of tiles ``warp``, warp + 2
+        constexpr int kOwn = C::kTiles / 2;
+        const uint32_t idesc_o = ptx::idesc_bf16_f32(128, D, false, true);
+        int i = 0;                              // blocks so far
+        int done[kOwn] = {}, use[kOwn] = {};    // of these, the tile's own; its units
+        bool ok = true;
+        // S = Q K^T of the unit's b-th block, the ``at``-th in all
+        auto qk = [&](const Unit& x, int y, int b, int at) -> bool {
+            const int tile = warp + 2 * y, c = done[y] + b, stage = at % kRing, buf = c % NB;
+            const uint32_t cols = tmem + (uint32_t)tile * C::kTileCols;
+            if (!warp_wait(&sb->kv_full[stage], (at / kRing) & 1, &sb->abort, status)) return false;
+            // the buffer's last S: read, or (P shares its columns) used by its P V
+            if (c >= NB && !warp_wait(C::kAlias ? &sb->o_done[tile][buf] : &sb->s_free[tile][buf], (c / NB - 1) & 1,
+                                      &sb->abort, status))
+                return false;
+            ptx::tc_fence_after();
+            const uint64_t qd = k_major<D>(sbase + (uint32_t)(tile * 2 + (use[y] & 1)) * C::kQTile);
+            const uint64_t kd = k_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile);
+            const uint32_t idesc = ptx::idesc_bf16_f32(128, block_cols<BN>(x.n, x.t0 + b), false, false);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::warp_mma_bf16(cols + (uint32_t)buf * 64u, qd + k_step<D>(kk, 128), kd + k_step<D>(kk, BN), idesc, kk);
-                ptx::warp_mma_commit(&sb->s_full[grp][buf]);
-                if (b == x.nb - 1) ptx::warp_mma_commit(&sb->q_empty[grp][use & 1]);
-                return true;
-            };
-            // O += P V
-            auto pv = [&](const Unit& x, int b, int at) -> bool {
-                const int stage = at % kRing, buf = at % NB;
-                if (!warp_wait(&sb->p_full[grp][buf], (at / NB) & 1, &sb->abort, status)) return false;
-                ptx::tc_fence_after();
-                const uint64_t vd = n_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile, BN);
-                const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
-                const uint32_t pt = cols + C::kP + (uint32_t)buf * 64u;
+            for (int kk = 0; kk < D / 16; ++kk)
+                ptx::warp_mma_bf16(cols + (uint32_t)buf * 64u, qd + k_step<D>(kk, 128), kd + k_step<D>(kk, BN), idesc, kk);
+            ptx::warp_mma_commit(&sb->s_full[tile][buf]);
+            if (b == x.nb - 1) ptx::warp_mma_commit(&sb->q_empty[tile][use[y] & 1]);
+            return true;
+        };
+        // O += P V
+        auto pv = [&](const Unit& x, int y, int b, int at) -> bool {
+            const int tile = warp + 2 * y, c = done[y] + b, stage = at % kRing, buf = c % NB;
+            const uint32_t cols = tmem + (uint32_t)tile * C::kTileCols;
+            if (!warp_wait(&sb->p_full[tile][buf], (c / NB) & 1, &sb->abort, status)) return false;
+            ptx::tc_fence_after();
+            const uint64_t vd = n_major<D>(sbase + C::kOffKv + (uint32_t)stage * 2u * C::kKvTile + C::kKvTile, BN);
+            const int steps = block_cols<BN>(x.n, x.t0 + b) >> 4;
+            const uint32_t pt = cols + C::kP + (uint32_t)buf * 64u;
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    if (kk < steps)
-                        ptx::warp_mma_bf16_ta(cols + C::kO, pt + (uint32_t)kk * 8u, vd + n_step<D>(kk), idesc_o,
-                                         kk > 0 ? 1u : (uint32_t)(b > 0));
-                ptx::warp_mma_commit(&sb->o_done[grp][buf]);
-                ptx::warp_mma_commit(&sb->kv_empty[stage]);
-                return true;
-            };
-            for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const Unit x = unit_at<BN>(g, p, u);
-                if (x.nb == 0) continue;
-                ok = warp_wait(&sb->q_full[grp][use & 1], (use >> 1) & 1, &sb->abort, status) && qk(x, 0, i);
-                for (int b = 0; ok && b < x.nb; ++b) ok = (b + 1 == x.nb || qk(x, b + 1, i + b + 1)) && pv(x, b, i + b);
-                i += x.nb;
-                ++use;
+            for (int kk = 0; kk < BN / 16; ++kk)
+                if (kk < steps)
+                    ptx::warp_mma_bf16_ta(cols + C::kO, pt + (uint32_t)kk * 8u, vd + n_step<D>(kk), idesc_o,
+                                          kk > 0 ? 1u : (uint32_t)(b > 0));
+            ptx::warp_mma_commit(&sb->o_done[tile][buf]);
+            ptx::warp_mma_commit(&sb->kv_empty[stage]);
+            return true;
+        };
+        for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
+            const Unit x = unit_at<BN, 128 * C::kTiles>(g, p, u);
+            bool on[kOwn];  // the tile has rows
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y) on[y] = x.row0 + (warp + 2 * y) * 128 < g.rows;
+            for (int b = -1; ok && b < x.nb; ++b) {
+#pragma unroll
+                for (int y = 0; y < kOwn; ++y) {
+                    if (!ok || !on[y] || b + 1 >= x.nb) continue;
+                    if (b < 0) ok = warp_wait(&sb->q_full[warp + 2 * y][use[y] & 1], (use[y] >> 1) & 1, &sb->abort, status);
+                    ok = ok && qk(x, y, b + 1, i + b + 1);
+                }
+                if (b < 0) continue;
+#pragma unroll
+                for (int y = 0; y < kOwn; ++y) {
+                    if (!ok) continue;
+                    if (on[y]) {
+                        ok = pv(x, y, b, i + b);
+                    } else {
+                        ok = warp_wait(&sb->kv_full[(i + b) % kRing], ((i + b) / kRing) & 1, &sb->abort, status);
+                        if (lane == 0) ptx::mbar_arrive(&sb->kv_empty[(i + b) % kRing]);
+                    }
+                }
             }
-            ptx::warp_mma_commit(&sb->drain[grp]);
-            ptx::mbar_wait(&sb->drain[grp], 0, kWait);
+            i += x.nb;
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y)
+                if (on[y] && x.nb > 0) {
+                    done[y] += x.nb;
+                    ++use[y];
+                }
         }
+        ptx::warp_mma_commit(&sb->drain[warp]);
+        ptx::mbar_wait(&sb->drain[warp], 0, kWait);
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------------ loads
@@ -209,19 +233,22 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             ptx::tma_prefetch_desc(&tk);
             ptx::tma_prefetch_desc(&tv);
         }
-        int i = 0, use = 0;
+        int i = 0, uses[C::kTiles] = {};
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at<BN>(g, p, u);
+            const Unit x = unit_at<BN, 128 * C::kTiles>(g, p, u);
             if (x.nb == 0) continue;
-            for (int grp = 0; grp < 2; ++grp) {
-                uint64_t* full = &sb->q_full[grp][use & 1];
-                if (use >= 2 && !warp_wait(&sb->q_empty[grp][use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) {
+#pragma unroll
+            for (int tile = 0; tile < C::kTiles; ++tile) {
+                const int row0 = x.row0 + tile * 128;
+                if (!ok || row0 >= g.rows) continue;
+                const int use = uses[tile]++;
+                uint64_t* full = &sb->q_full[tile][use & 1];
+                if (use >= 2 && !warp_wait(&sb->q_empty[tile][use & 1], ((use >> 1) - 1) & 1, &sb->abort, status)) {
                     ok = false;
-                    break;
+                    continue;
                 }
-                const uint32_t qt = sbase + (uint32_t)(grp * 2 + (use & 1)) * C::kQTile;
-                const int row0 = x.row0 + grp * 128;
+                const uint32_t qt = sbase + (uint32_t)(tile * 2 + (use & 1)) * C::kQTile;
                 if (p.tma_q) {
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(full, C::kQTile);
@@ -274,14 +301,13 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     if (lane == 0) ptx::mbar_arrive(land);
                 }
             }
-            ++use;
         }
     } else if (warp == 3) {
         // ---------------------------------------- landed blocks, passed to the products
         int i = 0;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at<BN>(g, p, u);
+            const Unit x = unit_at<BN, 128 * C::kTiles>(g, p, u);
             for (int b = 0; b < x.nb; ++b, ++i) {
                 const int stage = i % kRing;
                 if (!warp_wait(&sb->kv_land[stage], (i / kRing) & 1, &sb->abort, status)) {
@@ -298,21 +324,25 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         }
     } else {
         // ------------------------------------------------------ softmax + epilogue
-        const int grp = (warp - kCtrl) >> 2, qd = warp & 3;
+        const int tile = (warp - kCtrl) >> 2, qd = warp & 3;
         const int row = 32 * qd + lane;
-        const uint32_t cols = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)grp * C::kGroupCols;
+        const uint32_t cols = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)tile * C::kTileCols;
         const float sl = g.scale * kLog2e;
         const uint64_t sl2 = ptx::pack_f32x2(sl, sl);
-        int i = 0;  // blocks so far
+        int i = 0, done = 0;  // blocks so far; this tile's own
         bool ok = true;
         for (int u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-            const Unit x = unit_at<BN>(g, p, u);
+            const Unit x = unit_at<BN, 128 * C::kTiles>(g, p, u);
+            if (x.row0 + tile * 128 >= g.rows) {
+                i += x.nb;
+                continue;
+            }
             float m = -INFINITY;
             uint64_t l2 = 0ull;
-            for (int b = 0; b < x.nb; ++b, ++i) {
-                const int buf = i % NB, phase = i / NB;
+            for (int b = 0; b < x.nb; ++b, ++i, ++done) {
+                const int buf = done % NB, phase = done / NB;
                 const uint32_t scol = cols + (uint32_t)buf * 64u;
-                if (!warp_wait(&sb->s_full[grp][buf], phase & 1, &sb->abort, status)) {
+                if (!warp_wait(&sb->s_full[tile][buf], phase & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -323,7 +353,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 ptx::tmem_load(scol, r);
                 if constexpr (!C::kAlias) {
                     ptx::tc_fence_before();
-                    ptx::mbar_arrive(&sb->s_free[grp][buf]);
+                    ptx::mbar_arrive(&sb->s_free[tile][buf]);
                 }
                 const int left = x.n - (x.t0 + b) * BN;
                 if (g.kv_mask || left < BN) {
@@ -351,7 +381,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                             ptx::max3(mx[(e >> 1) & 3], __uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1]));
                 const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
                 // P's buffer: its last P V is done
-                if (i >= NB && !warp_wait(&sb->o_done[grp][buf], (phase - 1) & 1, &sb->abort, status)) {
+                if (done >= NB && !warp_wait(&sb->o_done[tile][buf], (phase - 1) & 1, &sb->abort, status)) {
                     ok = false;
                     break;
                 }
@@ -359,7 +389,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     m = mn;
                 } else if (__any_sync(0xffffffffu, mn > m + kGrow)) {
                     // O stands still once the previous block's P V is done
-                    if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) {
+                    if (!warp_wait(&sb->o_done[tile][(done - 1) % NB], ((done - 1) / NB) & 1, &sb->abort, status)) {
                         ok = false;
                         break;
                     }
@@ -410,17 +440,17 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&sb->p_full[grp][buf]);
+                ptx::mbar_arrive(&sb->p_full[tile][buf]);
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->o_done[grp][(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) break;
+                if (!warp_wait(&sb->o_done[tile][(done - 1) % NB], ((done - 1) / NB) & 1, &sb->abort, status)) break;
                 ptx::tc_fence_after();
             }
             float lo, hi;
             ptx::unpack_f32x2(l2, lo, hi);
             const float l = lo + hi;
-            const int r0 = x.row0 + grp * 128 + row;
+            const int r0 = x.row0 + tile * 128 + row;
             const bool in = r0 < g.rows;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const size_t part = ((size_t)(x.split * g.B + x.b) * g.kv_heads + x.j) * g.rows + r0;
@@ -478,7 +508,7 @@ bra_status launch_d(const CrossGeom& g, const TcPlan& plan, int grid, const void
     p.tma_kv = g.Lk >= C::kBlock && encode_heads_map(&tk, k, g.B, g.Lk, g.kv_heads, D, g.k_row, g.k_batch, C::kBlock, 1) &&
                encode_heads_map(&tv, v, g.B, g.Lk, g.kv_heads, D, g.v_row, g.v_batch, C::kBlock, 1);
     const cudaError_t e = launch_after_previous(
-        bra_cross_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv,
+        bra_cross_tc_kernel<D>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, tq, tk, tv,
         static_cast<const __nv_bfloat16*>(q),
         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o),
         lse, parts, g, p, status);
@@ -489,14 +519,14 @@ bra_status launch_d(const CrossGeom& g, const TcPlan& plan, int grid, const void
 
 bool cross_tc_covers(const CrossGeom& g) { return g.rows >= 128; }
 
-int cross_tc_rows() { return 256; }
+int cross_tc_rows(const CrossGeom& g) { return 128 * (g.d == 32 ? Cfg<32>::kTiles : Cfg<64>::kTiles); }
 
 bra_status cross_forward_tc(const CrossGeom& g, int splits, const void* q, const void* k, const void* v, void* o,
                             float* lse, CrossParts parts, int* status, cudaStream_t stream) {
     TcPlan p = {};
-    p.pairs = (g.rows + 255) / 256;
+    p.groups = (g.rows + cross_tc_rows(g) - 1) / cross_tc_rows(g);
     p.splits = splits;
-    const long long units = (long long)p.pairs * splits * g.kv_heads * g.B;
+    const long long units = (long long)p.groups * splits * g.kv_heads * g.B;
     if (units > 0x3fffffffLL) return BRA_ERR_UNSUPPORTED;
     p.units = (int)units;
     const int sms = sm_count();

@@ -10,8 +10,9 @@
 //           2^-9 |dO| |O| multiplies every state alike, so that in dQ it adds up
 //           to (D - D0) sum_j P_j k_j, ten times the roundings' share over
 //           some thousand states whose K has a mean.  Since sum_j P_j = 1, the
-//           fp32 row sum of P (dP - D0) is D - D0; with a second accumulator
-//           for sum_j P_j k_j the kernel takes the error out at its end;
+//           row sum of P (dP - D0) is D - D0; with a second accumulator for
+//           sum_j P_j k_j the kernel takes the error out at its end.  The sum is
+//           that of the rounded dS, so that the roundings' own sum goes with it;
 //   dK, dV  a CTA owns 64 states (four warps x 16) and streams the group's
 //           rows in tiles of 64, with the transposed scores S^T = K Q^T, so
 //           that P^T and dS^T are already the first operands of their products.
@@ -244,7 +245,7 @@ bra_cross_dq_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
                 for (int e = 0; e < 4; ++e) {
                     const bool on = (w >> (i * 8 + (lane & 3) * 2 + (e & 1))) & 1u;
                     const float p = on ? ptx::ex2(fmaf(s[i][e], c2, -lr[e >> 1])) : 0.f;
-                    s[i][e] = p * (dp[i][e] - dr[e >> 1]);
+                    s[i][e] = __bfloat162float(__float2bfloat16_rn(p * (dp[i][e] - dr[e >> 1])));
                     dp[i][e] = p;
                     rest[e >> 1] += s[i][e];
                 }

@@ -430,19 +430,23 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                                 lo, hi);
                             lo = ptx::ex2(lo);
                             hi = ptx::ex2(hi);
-                            uint64_t ds = ptx::mul_f32x2(
-                                ptx::pack_f32x2(lo, hi),
-                                ptx::add_f32x2(
-                                    ptx::pack_f32x2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), dd));
-                            ptx::unpack_f32x2(ds, dlo, dhi);
+                            ptx::unpack_f32x2(
+                                ptx::mul_f32x2(ptx::pack_f32x2(lo, hi),
+                                               ptx::add_f32x2(ptx::pack_f32x2(__uint_as_float(dp[2 * e]),
+                                                                              __uint_as_float(dp[2 * e + 1])),
+                                                              dd)),
+                                dlo, dhi);
                             if (masked) {  // nothing, whatever the columns hold
                                 if (!((w >> (2 * e)) & 1u)) lo = dlo = 0.f;
                                 if (!((w >> (2 * e + 1)) & 1u)) hi = dhi = 0.f;
-                                ds = ptx::pack_f32x2(dlo, dhi);
                             }
-                            if (!STATES) rest2 = ptx::add_f32x2(rest2, ds);
                             pp[e] = ptx::pack_bf16x2(lo, hi);
                             pd[e] = ptx::pack_bf16x2(dlo, dhi);
+                            // the sum of dS as it enters the product: taking it out of dQ takes the roundings' sum
+                            // out too, which would multiply what K's states have in common
+                            if (!STATES)
+                                rest2 = ptx::add_f32x2(rest2, ptx::pack_f32x2(__uint_as_float(pd[e] << 16),
+                                                                              __uint_as_float(pd[e] & 0xffff0000u)));
                         }
                     };
                     if (STATES || w == 0xffffu) form(false);

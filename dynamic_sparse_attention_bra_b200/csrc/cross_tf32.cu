@@ -1,7 +1,6 @@
 // Cross attention and its gradients in fp32 on tensor cores (the formulas are
-// those of the bf16 kernels).  Every fp32 factor x is split into the part that a
-// tf32 product reads, x with the 13 low bits cleared, and the rest, x - that,
-// which is exact; a product of two factors is then three tf32 products,
+// those of the bf16 kernels).  Every fp32 factor x is split into x rounded to tf32
+// and the rest, x - that, which is exact; a product of two factors is then three tf32 products,
 //   x y = xh yh + xh yl + xl yh  (+ xl yl, below 2^-20 of x y),
 // summed in fp32: some 2^-21 of relative error a factor, the order of fp32's own
 // roundings in a sum.  Three products cost 24 clocks of a warp's tensor unit for
@@ -25,7 +24,7 @@ using namespace cross;
 // ---------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
@@ -45,12 +44,13 @@ struct Split {
         split(a2, hi[2], lo[2]);
         split(a3, hi[3], lo[3]);
     }
-    __device__ __forceinline__ void times(float (&d)[4], float b0, float b1) const {
+    // d += the first parts' product, r += the two others
+    __device__ __forceinline__ void times(float (&d)[4], float (&r)[4], float b0, float b1) const {
         uint32_t h0, l0, h1, l1;
         split(b0, h0, l0);
         split(b1, h1, l1);
-        mma_tf32(d, lo, h0, h1);
-        mma_tf32(d, hi, l0, l1);
+        mma_tf32(r, lo, h0, h1);
+        mma_tf32(r, hi, l0, l1);
         mma_tf32(d, hi, h0, h1);
     }
 };
@@ -66,14 +66,15 @@ __device__ __forceinline__ float4 lds128(uint32_t at) {
     return v;
 }
 
-// s[i] += (16 rows of tile ``a`` from a0) x (rows b0 + 8 i .. of tile ``b``)^T
+// s[i] = (16 rows of tile ``a`` from a0) x (rows b0 + 8 i .. of tile ``b``)^T
 template <int D, int N>
 __device__ __forceinline__ void scores(uint32_t a, int a0, uint32_t b, int b0, int lane, float (&s)[N][4]) {
     const int gq = lane >> 2, t4 = lane & 3;
+    float r[N][4];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[i][e] = r[i][e] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
         const float4 x = lds128(a + f32_offset<D>(a0 + gq, c * 4 + t4)), y = lds128(a + f32_offset<D>(a0 + 8 + gq, c * 4 + t4));
@@ -83,43 +84,48 @@ __device__ __forceinline__ void scores(uint32_t a, int a0, uint32_t b, int b0, i
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float4 z = lds128(b + f32_offset<D>(b0 + 8 * i + gq, c * 4 + t4));
-            f[0].times(s[i], z.x, z.y);
-            f[1].times(s[i], z.z, z.w);
+            f[0].times(s[i], r[i], z.x, z.y);
+            f[1].times(s[i], r[i], z.z, z.w);
         }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] += r[i][e];
 }
 
 // acc += p (16 rows x 8 N columns, as scores leaves them) x (8 N rows of ``tile`` from row0).
 // acc[4 m + x]: channels 32 m + 8 t + x (first of each pair) and + 4 (second).
 // The tensor unit cuts off what falls below its sum, always towards zero: over some
 // hundred products into one sum that is a bias of 2^-18.  So a tile's products make
-// a sum of their own (3 N products), added to acc in fp32, rounded to nearest.
+// sums of their own, of N products the first parts' and of 2 N the small others',
+// which are added to acc in fp32, rounded to nearest.
 template <int D, int N>
 __device__ __forceinline__ void accumulate(const float (&p)[N][4], uint32_t tile, int row0, int lane,
                                            float (&acc)[D / 8][4]) {
     const int gq = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int m = 0; m < D / 32; ++m) {
-        float sum[4][4];
+        float sum[4][4], low[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[x][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sum[x][e] = low[x][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             Split f;
             f.set(p[i][0], p[i][2], p[i][1], p[i][3]);
             const int r = row0 + 8 * i + 2 * t4;
             const float4 x = lds128(tile + f32_offset<D>(r, m * 8 + gq)), y = lds128(tile + f32_offset<D>(r + 1, m * 8 + gq));
-            f.times(sum[0], x.x, y.x);
-            f.times(sum[1], x.y, y.y);
-            f.times(sum[2], x.z, y.z);
-            f.times(sum[3], x.w, y.w);
+            f.times(sum[0], low[0], x.x, y.x);
+            f.times(sum[1], low[1], x.y, y.y);
+            f.times(sum[2], low[2], x.z, y.z);
+            f.times(sum[3], low[3], x.w, y.w);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[4 * m + x][e] += sum[x][e];
+            for (int e = 0; e < 4; ++e) acc[4 * m + x][e] += sum[x][e] + low[x][e];
     }
 }
 

@@ -440,13 +440,14 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 
 }  // namespace
 
-// Enough row splits for two CTAs on each SM, each of at least four row tiles.
+// Enough row splits for two CTAs on each SM (fp32: three at d = 32, one CTA
+// of twice the warps otherwise), each of at least four row tiles.
 int cross_backward_splits(const CrossGeom& g, bool bf16) {
     if (bf16 && cross_tc_backward_covers(g)) return cross_tc_backward_splits(g);
-    const int sms = sm_count();
+    const int slots = sm_count() * (bf16 ? 2 : g.d == 32 ? 3 : 1);
     const long long ctas = (long long)((g.Lk + 63) / 64) * g.kv_heads * g.B;
-    if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return 1;
-    long long s = 2LL * sms / ctas;
+    if (slots <= 0 || ctas <= 0 || ctas >= slots) return 1;
+    long long s = slots / ctas;
     const long long most = ((g.rows + 63) / 64) / 4;
     if (s > most) s = most;
     return s < 1 ? 1 : (int)s;

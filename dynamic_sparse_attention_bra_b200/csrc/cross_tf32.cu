@@ -24,7 +24,7 @@ using namespace cross;
 // ---------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // (integer operations: conversions run at a quarter of their rate)
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
@@ -94,18 +94,19 @@ __device__ __forceinline__ void scores(uint32_t a, int a0, uint32_t b, int b0, i
         for (int e = 0; e < 4; ++e) s[i][e] += r[i][e];
 }
 
-// acc += p (16 rows x 8 N columns, as scores leaves them) x (8 N rows of ``tile`` from row0).
-// acc[4 m + x]: channels 32 m + 8 t + x (first of each pair) and + 4 (second).
+// acc += p (16 rows x 8 N columns, as scores leaves them) x (8 N rows of ``tile`` from row0),
+// for the MC blocks of 32 channels from m0: acc[4 m + x] has the channels
+// 32 (m0 + m) + 8 t + x (first of each pair) and + 4 (second).
 // The tensor unit cuts off what falls below its sum, always towards zero: over some
 // hundred products into one sum that is a bias of 2^-18.  So a tile's products make
 // sums of their own, of N products the first parts' and of 2 N the small others',
 // which are added to acc in fp32, rounded to nearest.
-template <int D, int N>
-__device__ __forceinline__ void accumulate(const float (&p)[N][4], uint32_t tile, int row0, int lane,
-                                           float (&acc)[D / 8][4]) {
+template <int D, int N, int MC>
+__device__ __forceinline__ void accumulate(const float (&p)[N][4], uint32_t tile, int row0, int m0, int lane,
+                                           float (&acc)[4 * MC][4]) {
     const int gq = lane >> 2, t4 = lane & 3;
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) {
+    for (int m = 0; m < MC; ++m) {
         float sum[4][4], low[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -115,8 +116,8 @@ __device__ __forceinline__ void accumulate(const float (&p)[N][4], uint32_t tile
         for (int i = 0; i < N; ++i) {
             Split f;
             f.set(p[i][0], p[i][2], p[i][1], p[i][3]);
-            const int r = row0 + 8 * i + 2 * t4;
-            const float4 x = lds128(tile + f32_offset<D>(r, m * 8 + gq)), y = lds128(tile + f32_offset<D>(r + 1, m * 8 + gq));
+            const int r = row0 + 8 * i + 2 * t4, c = (m0 + m) * 8 + gq;
+            const float4 x = lds128(tile + f32_offset<D>(r, c)), y = lds128(tile + f32_offset<D>(r + 1, c));
             f.times(sum[0], low[0], x.x, y.x);
             f.times(sum[1], low[1], x.y, y.y);
             f.times(sum[2], low[2], x.z, y.z);
@@ -130,9 +131,9 @@ __device__ __forceinline__ void accumulate(const float (&p)[N][4], uint32_t tile
 }
 
 // The same with the factors' first parts alone (2^-10), for what need not be exact.
-template <int D, int N>
-__device__ __forceinline__ void accumulate_coarse(const float (&p)[N][4], uint32_t tile, int row0, int lane,
-                                                  float (&acc)[D / 8][4]) {
+template <int D, int N, int MC>
+__device__ __forceinline__ void accumulate_coarse(const float (&p)[N][4], uint32_t tile, int row0, int m0, int lane,
+                                                  float (&acc)[4 * MC][4]) {
     const int gq = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -140,8 +141,9 @@ __device__ __forceinline__ void accumulate_coarse(const float (&p)[N][4], uint32
                                __float_as_uint(p[i][3])};
         const int r = row0 + 8 * i + 2 * t4;
 #pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
-            const float4 x = lds128(tile + f32_offset<D>(r, m * 8 + gq)), y = lds128(tile + f32_offset<D>(r + 1, m * 8 + gq));
+        for (int m = 0; m < MC; ++m) {
+            const int c = (m0 + m) * 8 + gq;
+            const float4 x = lds128(tile + f32_offset<D>(r, c)), y = lds128(tile + f32_offset<D>(r + 1, c));
             mma_tf32(acc[4 * m], a, __float_as_uint(x.x), __float_as_uint(y.x));
             mma_tf32(acc[4 * m + 1], a, __float_as_uint(x.y), __float_as_uint(y.y));
             mma_tf32(acc[4 * m + 2], a, __float_as_uint(x.z), __float_as_uint(y.z));
@@ -150,19 +152,19 @@ __device__ __forceinline__ void accumulate_coarse(const float (&p)[N][4], uint32
     }
 }
 
-template <int D>
-__device__ __forceinline__ void zero(float (&acc)[D / 8][4]) {
+template <int N>
+__device__ __forceinline__ void zero(float (&acc)[N][4]) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 }
 
-// Row h (0: gq, 1: gq + 8) of acc, times f, to D floats at ``row``: 32 bytes of every 32 channels a thread.
-template <int D>
-__device__ __forceinline__ void store_row(float* row, const float (&acc)[D / 8][4], int h, float f, int t4) {
+// Row h (0: gq, 1: gq + 8) of acc, times f, to its channels of ``row``: 32 bytes of every 32 channels a thread.
+template <int N>
+__device__ __forceinline__ void store_row(float* row, const float (&acc)[N][4], int h, float f, int t4) {
 #pragma unroll
-    for (int m = 0; m < D / 32; ++m) {
+    for (int m = 0; m < N / 4; ++m) {
         float4* dst = reinterpret_cast<float4*>(row + 32 * m + 8 * t4);
         dst[0] = make_float4(acc[4 * m][2 * h] * f, acc[4 * m + 1][2 * h] * f, acc[4 * m + 2][2 * h] * f,
                              acc[4 * m + 3][2 * h] * f);
@@ -249,7 +251,7 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
     fetch(t0);
     const float sl = g.scale * kLog2e;
     float acc[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    zero<D>(acc);
+    zero(acc);
     for (int t = t0; t < t1; ++t) {
         ptx::cp_async_wait_group<0>();
         __syncthreads();  // this tile has landed, and everyone is done with the last
@@ -292,7 +294,7 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
                 acc[i][2 * h + 1] *= alpha;
             }
         }
-        accumulate<D, N>(s, st + tile_bytes<D>(), wn * KW, lane, acc);
+        accumulate<D, N, D / 32>(s, st + tile_bytes<D>(), wn * KW, 0, lane, acc);
     }
     ptx::cp_async_wait_all();
     allow_dependents();
@@ -308,7 +310,7 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = wn * S::kRows + wm * 16 + h * 8 + gq;
-            store_row<D>(jo + (size_t)r * D, acc, h, 1.f, t4);
+            store_row(jo + (size_t)r * D, acc, h, 1.f, t4);
             if (t4 == 0) {
                 jm[r * 2] = m[h];
                 jm[r * 2 + 1] = l[h];
@@ -352,10 +354,10 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
             if (r >= g.rows) continue;
             if (splits > 1) {
                 const size_t at = ((size_t)(split * g.B + b) * g.kv_heads + j) * g.rows + r;
-                store_row<D>(parts.o + at * D, acc, h, 1.f, t4);
+                store_row(parts.o + at * D, acc, h, 1.f, t4);
                 if (t4 == 0) parts.ml[at] = make_float2(m[h], l[h]);
             } else {
-                store_row<D>(o + cross_o_offset(g, b, j, r), acc, h, l[h] > 0.f ? 1.f / l[h] : 0.f, t4);
+                store_row(o + cross_o_offset(g, b, j, r), acc, h, l[h] > 0.f ? 1.f / l[h] : 0.f, t4);
                 if (t4 == 0 && lse)
                     lse[cross_lse_offset(g, b, j, r)] = l[h] > 0.f ? (m[h] + log2f(l[h])) * kLn2 : -INFINITY;
             }
@@ -363,34 +365,82 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
     }
 }
 
-// ------------------------------------------------------------------ dQ and D
-// <dO, O> is D0; what it lacks to D multiplies sum_j P_j k_j in dQ and is taken out
-// at the end, as in the bf16 kernel: O's 2^-20 would make 10^-5 of dQ over 8000
-// states.  That sum needs no second parts.
-constexpr int kThreads = 128;
-
-// shared memory: Q | dO | ring of 2 x (K | V) | D, log sums [64] | mask bits
-template <int D>
-constexpr uint32_t dq_smem() { return 6u * tile_bytes<D>() + 512u + 2u * ValidBits::kWords * 4u; }
+// ----------------------------------------------------------------- gradients
+// Eight warps: 16 rows of a tile of 64 each pair, and of a pair each warp the scores
+// of 32 columns.  d = 32: it also sums over these, and the pair joins its sums at the
+// end.  d = 64, 128: registers do not hold the sums of all channels, so the pair
+// exchanges P and dS through shared memory, in fragment order, and each warp sums half
+// of the channels over all 64 columns.
+constexpr int kThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+struct Grad {
+    static constexpr bool kExchange = D > 32;
+    static constexpr int kBlocks = kExchange ? D / 64 : 1;  // of 32 channels that a warp sums
+    static constexpr uint32_t kShare = 4u * 8u * 32u * 16u;  // one exchanged matrix (or the join's sums)
+    // four tiles, or the rows' two and a ring of two stages of two | exchange | statistics | mask bits
+    static constexpr uint32_t kOffShare = 6u * tile_bytes<D>();
+    static constexpr uint32_t kOffStat = kOffShare + 2u * kShare;
+    static constexpr uint32_t kBytes = kOffStat + 1024u + 2u * ValidBits::kWords * 4u;
+    static_assert(kBytes <= 227u * 1024u, "shared memory");
+};
+
+// This warp's 16 x 32 part of a matrix to, or the pair's 16 x 64 from, shared memory.
+__device__ __forceinline__ void give(uint32_t share, int pair, int half, int lane, const float (&s)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        ptx::st_shared_v4(share + (uint32_t)(((pair * 8 + half * 4 + i) * 32 + lane) * 16), __float_as_uint(s[i][0]),
+                          __float_as_uint(s[i][1]), __float_as_uint(s[i][2]), __float_as_uint(s[i][3]));
+}
+__device__ __forceinline__ void take(uint32_t share, int pair, int lane, float (&s)[8][4]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 v = lds128(share + (uint32_t)(((pair * 8 + i) * 32 + lane) * 16));
+        s[i][0] = v.x;
+        s[i][1] = v.y;
+        s[i][2] = v.z;
+        s[i][3] = v.w;
+    }
+}
+// d = 32: the right warp's sums (4 x 4 a thread) added to the left's; the whole CTA calls it.
+__device__ __forceinline__ void join_pair(uint32_t share, int pair, int half, int lane, float (&acc)[4][4]) {
+    if (half == 1) give(share, pair, 0, lane, acc);
+    __syncthreads();
+    if (half == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = lds128(share + (uint32_t)(((pair * 8 + i) * 32 + lane) * 16));
+            acc[i][0] += v.x;
+            acc[i][1] += v.y;
+            acc[i][2] += v.z;
+            acc[i][3] += v.w;
+        }
+    }
+}
+
+// dQ and D.  <dO, O> is D0; what it lacks to D multiplies sum_j P_j k_j in dQ and is
+// taken out at the end, as in the bf16 kernel: O's 2^-20 would make 10^-5 of dQ over
+// 8000 states.  That sum needs no second parts.
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 32 ? 2 : 1)
 bra_cross_tf32_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                          const float* __restrict__ o, const float* lse, const float* __restrict__ go,
                          float* __restrict__ dq, float* delta, CrossGeom g, int row_tiles) {
+    using G = Grad<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr uint32_t kTile = tile_bytes<D>();
-    const uint32_t sq = ptx::smem_addr(smem), sg = sq + kTile, ring = sg + kTile;
-    float* sd = reinterpret_cast<float*>(smem + 6 * kTile);
+    const uint32_t sq = ptx::smem_addr(smem), sg = sq + kTile, ring = sg + kTile, share = sq + G::kOffShare;
+    float* sd = reinterpret_cast<float*>(smem + G::kOffStat);  // D0, -, log sums; at the end a row's two sums of dS
     float* sl = sd + 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
+    const int pair = warp & 3, half = warp >> 2;
     int id = blockIdx.x;
     const int row0 = (id % row_tiles) * 64;
     id /= row_tiles;
     const int j = id % g.kv_heads, b = id / g.kv_heads;
     grid_dependency_wait();
     const int n = cross_len(g, b), tiles = (n + 63) / 64;
-    ValidBits bits{reinterpret_cast<uint32_t*>(smem + 6 * kTile + 512),
+    ValidBits bits{reinterpret_cast<uint32_t*>(smem + G::kOffStat + 1024u),
                    g.kv_mask ? g.kv_mask + (size_t)b * g.Lk : nullptr, n};
     load_rows_f32<D, kThreads, 64>(sq, q, g, b, j, row0, false);
     load_rows_f32<D, kThreads, 64>(sg, go, g, b, j, row0, true);
@@ -405,13 +455,13 @@ bra_cross_tf32_dq_kernel(const float* __restrict__ q, const float* __restrict__ 
         ptx::cp_async_commit();
     };
     fetch(0);
-    {  // D and the log sums: two threads a row
-        const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
+    {  // D0 and the log sums: four threads a row
+        const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
         float x = 0.f;
         if (row0 + r < g.rows) {
-            const size_t off = cross_o_offset(g, b, j, row0 + r) + half * (D / 2);
+            const size_t off = cross_o_offset(g, b, j, row0 + r) + part * (D / 4);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
+            for (int c = 0; c < D / 16; ++c) {
                 const float4 f = __ldcg(reinterpret_cast<const float4*>(o + off) + c);
                 const float4 h = __ldcg(reinterpret_cast<const float4*>(go + off) + c);
                 x = fmaf(f.x, h.x, x);
@@ -421,83 +471,94 @@ bra_cross_tf32_dq_kernel(const float* __restrict__ q, const float* __restrict__ 
             }
         }
         x += __shfl_xor_sync(0xffffffffu, x, 1);
-        if (half == 0) {
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (part == 0) {
             sd[r] = x;
-            float ls = -INFINITY;
-            if (row0 + r < g.rows) {
-                ls = __ldcg(lse + cross_lse_offset(g, b, j, row0 + r));
-            }
-            sl[r] = exponent_offset(ls);
+            sl[r] = exponent_offset(row0 + r < g.rows ? __ldcg(lse + cross_lse_offset(g, b, j, row0 + r)) : -INFINITY);
         }
     }
     const float c2 = g.scale * kLog2e;
-    float acc[D / 8][4], mean[D / 8][4], rest[2] = {0.f, 0.f};
-    zero<D>(acc);
-    zero<D>(mean);
+    float acc[4 * G::kBlocks][4], mean[4 * G::kBlocks][4], rest[2] = {0.f, 0.f};
+    zero(acc);
+    zero(mean);
     for (int t = 0; t < tiles; ++t) {
         ptx::cp_async_wait_group<0>();
         __syncthreads();
         fetch(t + 1);
         const uint32_t st = ring + (uint32_t)(t & 1) * 2u * kTile;
+        const uint32_t w = bits.word(t, half);
+        if (!G::kExchange && w == 0u) continue;
+        float s[4][4], dp[4][4];
+        scores<D, 4>(sq, pair * 16, st, half * 32, lane, s);
+        scores<D, 4>(sg, pair * 16, st + kTile, half * 32, lane, dp);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t w = bits.word(t, hf);
-            if (w == 0u) continue;
-            float s[4][4], dp[4][4];
-            scores<D, 4>(sq, warp * 16, st, hf * 32, lane, s);
-            scores<D, 4>(sg, warp * 16, st + kTile, hf * 32, lane, dp);
+        for (int e = 0; e < 4; ++e) {
+            const int r = pair * 16 + (e >> 1) * 8 + gq;
+            const float off = sl[r], dd = sd[r];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = warp * 16 + (e >> 1) * 8 + gq;
-                const float off = sl[r], dd = sd[r];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool on = (w >> (i * 8 + t4 * 2 + (e & 1))) & 1u;
-                    const float p = on ? ptx::ex2(fmaf(s[i][e], c2, -off)) : 0.f;
-                    s[i][e] = p * (dp[i][e] - dd);
-                    dp[i][e] = p;
-                    rest[e >> 1] += s[i][e];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const bool on = (w >> (i * 8 + t4 * 2 + (e & 1))) & 1u;
+                const float p = on ? ptx::ex2(fmaf(s[i][e], c2, -off)) : 0.f;
+                s[i][e] = p * (dp[i][e] - dd);
+                dp[i][e] = p;
+                rest[e >> 1] += s[i][e];
             }
-            accumulate<D, 4>(s, st, hf * 32, lane, acc);
-            accumulate_coarse<D, 4>(dp, st, hf * 32, lane, mean);
+        }
+        if constexpr (G::kExchange) {
+            give(share, pair, half, lane, s);
+            give(share + G::kShare, pair, half, lane, dp);
+            __syncthreads();
+            float x[8][4];
+            take(share, pair, lane, x);
+            accumulate<D, 8, G::kBlocks>(x, st, 0, half * G::kBlocks, lane, acc);
+            take(share + G::kShare, pair, lane, x);
+            accumulate_coarse<D, 8, G::kBlocks>(x, st, 0, half * G::kBlocks, lane, mean);
+        } else {
+            accumulate<D, 4, 1>(s, st, half * 32, 0, lane, acc);
+            accumulate_coarse<D, 4, 1>(dp, st, half * 32, 0, lane, mean);
         }
     }
     ptx::cp_async_wait_all();
     allow_dependents();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {  // the row's sum of dS over both warps' columns
         rest[h] += __shfl_xor_sync(0xffffffffu, rest[h], 1);
         rest[h] += __shfl_xor_sync(0xffffffffu, rest[h], 2);
+        if (t4 == 0) sl[64 + half * 64 + pair * 16 + h * 8 + gq] = rest[h];
+    }
+    __syncthreads();
+    if constexpr (!G::kExchange) {
+        join_pair(share, pair, half, lane, acc);
+        join_pair(share + G::kShare, pair, half, lane, mean);
+        if (half == 1) return;
+    }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+    for (int h = 0; h < 2; ++h) {
+        const int y = pair * 16 + h * 8 + gq, r = row0 + y;
+        const float left = sl[64 + y] + sl[128 + y];
 #pragma unroll
-            for (int e = 2 * h; e < 2 * h + 2; ++e) acc[i][e] = fmaf(-rest[h], mean[i][e], acc[i][e]);
-        const int r = row0 + warp * 16 + h * 8 + gq;
+        for (int i = 0; i < 4 * G::kBlocks; ++i)
+#pragma unroll
+            for (int e = 2 * h; e < 2 * h + 2; ++e) acc[i][e] = fmaf(-left, mean[i][e], acc[i][e]);
         if (r >= g.rows) continue;
-        store_row<D>(dq + cross_o_offset(g, b, j, r), acc, h, g.scale, t4);
-        if (t4 == 0) delta[cross_lse_offset(g, b, j, r)] = sd[warp * 16 + h * 8 + gq] + rest[h];
+        store_row(dq + cross_o_offset(g, b, j, r) + half * G::kBlocks * 32, acc, h, g.scale, t4);
+        if (t4 == 0 && half == 0) delta[cross_lse_offset(g, b, j, r)] = sd[y] + left;
     }
 }
 
-// -------------------------------------------------------------------- dK, dV
-// shared memory: K | V | ring of R x (Q | dO) | R x (log sums, D) [64]
+// dK, dV: the rows are 64 states, the columns the group's rows of queries.
 template <int D>
-constexpr int kDkvRing = D == 128 ? 1 : 2;
-template <int D>
-constexpr uint32_t dkv_smem() { return (2u + 2u * kDkvRing<D>) * tile_bytes<D>() + kDkvRing<D> * 512u; }
-
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, D == 32 ? 2 : 1)
 bra_cross_tf32_dkv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                           const float* lse, const float* __restrict__ go, const float* delta, float* __restrict__ dk,
                           float* __restrict__ dv, float* parts, CrossGeom g, int key_tiles, int splits) {
+    using G = Grad<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr uint32_t kTile = tile_bytes<D>();
-    constexpr int kRing = kDkvRing<D>;
-    const uint32_t sk = ptx::smem_addr(smem), sv = sk + kTile, ring = sv + kTile;
-    float* stat = reinterpret_cast<float*>(smem + (2 + 2 * kRing) * kTile);
+    const uint32_t sk = ptx::smem_addr(smem), sv = sk + kTile, ring = sv + kTile, share = sk + G::kOffShare;
+    float* stat = reinterpret_cast<float*>(smem + G::kOffStat);  // [stage] (log sums, D) [64]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
+    const int pair = warp & 3, half = warp >> 2;
     int id = blockIdx.x;
     const int kt = id % key_tiles;
     id /= key_tiles;
@@ -519,15 +580,17 @@ bra_cross_tf32_dkv_kernel(const float* __restrict__ q, const float* __restrict__
     load_states_f32<D, kThreads>(sv, v + (size_t)b * g.v_batch + (size_t)j * D, g.v_row, kt, w[0], w[1]);
     auto fetch = [&](int t) {
         if (t < t1) {
-            const int x = (t - t0) % kRing;
+            const int x = (t - t0) & 1;
             const uint32_t st = ring + (uint32_t)x * 2u * kTile;
             load_rows_f32<D, kThreads, 64>(st, q, g, b, j, t * 64, false);
             load_rows_f32<D, kThreads, 64>(st + kTile, go, g, b, j, t * 64, true);
-            const int r = threadIdx.x & 63;  // a row's log sum (first 64 threads) or D
-            const bool in = t * 64 + r < g.rows;
-            const float* src = threadIdx.x < 64 ? lse : delta;
-            ptx::cp_async4(ptx::smem_addr(stat) + (uint32_t)(x * 128 + (int)threadIdx.x) * 4u,
-                           src + (in ? cross_lse_offset(g, b, j, t * 64 + r) : 0), in ? 4u : 0u);
+            if (threadIdx.x < 128) {  // a row's log sum (first 64 threads) or D
+                const int r = threadIdx.x & 63;
+                const bool in = t * 64 + r < g.rows;
+                const float* src = threadIdx.x < 64 ? lse : delta;
+                ptx::cp_async4(ptx::smem_addr(stat) + (uint32_t)(x * 128 + (int)threadIdx.x) * 4u,
+                               src + (in ? cross_lse_offset(g, b, j, t * 64 + r) : 0), in ? 4u : 0u);
+            }
         }
         ptx::cp_async_commit();
     };
@@ -535,58 +598,67 @@ bra_cross_tf32_dkv_kernel(const float* __restrict__ q, const float* __restrict__
     bool on[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int r = warp * 16 + h * 8 + gq;
+        const int r = pair * 16 + h * 8 + gq;
         on[h] = ((r < 32 ? w[0] : w[1]) >> (r & 31)) & 1u;
     }
     const float c2 = g.scale * kLog2e;
-    float ak[D / 8][4], av[D / 8][4];
-    zero<D>(ak);
-    zero<D>(av);
+    float ak[4 * G::kBlocks][4], av[4 * G::kBlocks][4];
+    zero(ak);
+    zero(av);
     for (int t = t0; t < t1; ++t) {
         ptx::cp_async_wait_group<0>();
         __syncthreads();
-        if (kRing > 1) fetch(t + 1);
-        const int x = (t - t0) % kRing;
+        fetch(t + 1);
+        const int x = (t - t0) & 1;
         const uint32_t st = ring + (uint32_t)x * 2u * kTile;
         const float* sl = stat + x * 128;
+        float s[4][4], dp[4][4];
+        scores<D, 4>(sk, pair * 16, st, half * 32, lane, s);
+        scores<D, 4>(sv, pair * 16, st + kTile, half * 32, lane, dp);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float s[4][4], dp[4][4];
-            scores<D, 4>(sk, warp * 16, st, hf * 32, lane, s);
-            scores<D, 4>(sv, warp * 16, st + kTile, hf * 32, lane, dp);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int y = 0; y < 2; ++y) {
+                const int col = half * 32 + i * 8 + t4 * 2 + y;
+                const float off = exponent_offset(sl[col]), dd = sl[64 + col];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int col = hf * 32 + i * 8 + t4 * 2 + y;
-                    const float off = exponent_offset(sl[col]), dd = sl[64 + col];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float p = on[h] ? ptx::ex2(fmaf(s[i][2 * h + y], c2, -off)) : 0.f;
-                        s[i][2 * h + y] = p;
-                        dp[i][2 * h + y] = p * (dp[i][2 * h + y] - dd);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const float p = on[h] ? ptx::ex2(fmaf(s[i][2 * h + y], c2, -off)) : 0.f;
+                    s[i][2 * h + y] = p;
+                    dp[i][2 * h + y] = p * (dp[i][2 * h + y] - dd);
                 }
-            accumulate<D, 4>(s, st + kTile, hf * 32, lane, av);
-            accumulate<D, 4>(dp, st, hf * 32, lane, ak);
-        }
-        if (kRing == 1) {
+            }
+        if constexpr (G::kExchange) {
+            give(share, pair, half, lane, s);
+            give(share + G::kShare, pair, half, lane, dp);
             __syncthreads();
-            fetch(t + 1);
+            float f[8][4];
+            take(share, pair, lane, f);
+            accumulate<D, 8, G::kBlocks>(f, st + kTile, 0, half * G::kBlocks, lane, av);
+            take(share + G::kShare, pair, lane, f);
+            accumulate<D, 8, G::kBlocks>(f, st, 0, half * G::kBlocks, lane, ak);
+        } else {
+            accumulate<D, 4, 1>(s, st + kTile, half * 32, 0, lane, av);
+            accumulate<D, 4, 1>(dp, st, half * 32, 0, lane, ak);
         }
     }
     ptx::cp_async_wait_all();
     allow_dependents();
+    if constexpr (!G::kExchange) {
+        join_pair(share, pair, half, lane, ak);
+        join_pair(share + G::kShare, pair, half, lane, av);
+        if (half == 1) return;
+    }
     const size_t elems = (size_t)g.B * g.Lk * g.kv_heads * D;
     float* ok = splits > 1 ? parts + (size_t)split * 2 * elems : dk;
     float* ov = splits > 1 ? ok + elems : dv;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int key = kt * 64 + warp * 16 + h * 8 + gq;
+        const int key = kt * 64 + pair * 16 + h * 8 + gq;
         if (key >= g.Lk) continue;
-        const size_t at = (((size_t)b * g.Lk + key) * g.kv_heads + j) * D;
-        store_row<D>(ok + at, ak, h, g.scale, t4);
-        store_row<D>(ov + at, av, h, 1.f, t4);
+        const size_t at = (((size_t)b * g.Lk + key) * g.kv_heads + j) * D + half * G::kBlocks * 32;
+        store_row(ok + at, ak, h, g.scale, t4);
+        store_row(ov + at, av, h, 1.f, t4);
     }
 }
 
@@ -618,18 +690,18 @@ bra_status backward_d(const CrossGeom& g, int splits, const void* q, const void*
                       const float* lse, const void* go, void* dq, void* dk, void* dv, float* delta, float* parts,
                       cudaStream_t stream) {
     using T = float;
-    if (!allow_shared<bra_cross_tf32_dq_kernel<D>>(dq_smem<D>()) || !allow_shared<bra_cross_tf32_dkv_kernel<D>>(dkv_smem<D>()))
+    if (!allow_shared<bra_cross_tf32_dq_kernel<D>>(Grad<D>::kBytes) || !allow_shared<bra_cross_tf32_dkv_kernel<D>>(Grad<D>::kBytes))
         return BRA_ERR_CUDA;
     const int row_tiles = (g.rows + 63) / 64, key_tiles = (g.Lk + 63) / 64;
     const long long grid_q = (long long)row_tiles * g.kv_heads * g.B;
     const long long grid_k = (long long)key_tiles * splits * g.kv_heads * g.B;
     if (grid_q > 0x7fffffffLL || grid_k > 0x7fffffffLL) return BRA_ERR_UNSUPPORTED;
     cudaError_t e = launch_after_previous(bra_cross_tf32_dq_kernel<D>, dim3((unsigned)grid_q), dim3(kThreads),
-                                          dq_smem<D>(), stream, (const T*)q, (const T*)k, (const T*)v, (const T*)o,
+                                          Grad<D>::kBytes, stream, (const T*)q, (const T*)k, (const T*)v, (const T*)o,
                                           lse, (const T*)go, (T*)dq, delta, g, row_tiles);
     if (e != cudaSuccess) return BRA_ERR_CUDA;
     if (grid_k == 0) return BRA_OK;
-    e = launch_after_previous(bra_cross_tf32_dkv_kernel<D>, dim3((unsigned)grid_k), dim3(kThreads), dkv_smem<D>(),
+    e = launch_after_previous(bra_cross_tf32_dkv_kernel<D>, dim3((unsigned)grid_k), dim3(kThreads), Grad<D>::kBytes,
                               stream, (const T*)q, (const T*)k, (const T*)v, lse, (const T*)go, (const float*)delta,
                               (T*)dk, (T*)dv, parts, g, key_tiles, splits);
     return e == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;

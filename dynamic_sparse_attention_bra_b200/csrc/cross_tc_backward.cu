@@ -12,12 +12,13 @@
 //   dK += dS Q,   dV += P dO                (rows of states)
 // whose sums stay in TMEM over all blocks.
 //
-// S and dP have two buffers (256 columns; the sums take 2 d of the others), so
-// that the products of the next block run under the exponentials of this one (d =
-// 32: one buffer, and two CTAs on an SM, which also hide the ends of short units).
-// There is no maximum to agree on, so two threads share a row, in parts of 16
-// columns, and (d >= 64) two groups of such threads take the blocks in turn: a
-// block's waits and TMEM latencies cost its threads as much as its arithmetic.
+// S and dP have buffers for the blocks ahead (two at d = 128, three at d = 64:
+// what the sums' 2 d columns leave), so that the products of the next block run
+// under the exponentials of this one.  At d = 32 one buffer and two CTAs on an SM do
+// the same, and hide the ends of short units as well (64 entries of 784 rows over 196
+// states, 4 heads: 106 us for 125).  There is no maximum to agree on, so several
+// threads share a row, in parts of 16 columns: four at d = 64; two, and at d = 128 two
+// groups of such threads that take the blocks in turn, elsewhere.
 // Roles of the warps: 0 issues S and dP, 1 the sums' products; 2 starts the loads
 // (TMA, or cp.async where no map can be made); 3 passes each landed tile on, after
 // it has zeroed the rows of masked or missing states (what is stored there must
@@ -46,7 +47,7 @@ struct Barriers {
     uint64_t c_land[kStages], c_full[kStages], c_empty[kStages];
     uint64_t r_land[2], r_full[2], r_empty[2];
     uint64_t s_full[3], p_full[3], acc_done[3];  // [buffer]
-    uint64_t rest_full, epi_done, drain[2];
+    uint64_t unit_done, rest_full, epi_done, drain[2];
     uint32_t words[kStages][2];  // dQ: the block's valid states
     uint32_t row_words[2][4];    // dK, dV: the tile's
     uint32_t tmem;
@@ -57,8 +58,9 @@ template <int D>
 struct Cfg {
     static constexpr int kCtas = D == 32 ? 2 : 1;   // on an SM
     static constexpr int kBufs = D == 32 ? 1 : D == 64 ? 3 : 2;  // of S and dP
-    static constexpr int kGroups = D == 32 ? 1 : 2;  // of row threads, taking blocks in turn
-    static constexpr int kShare = 2;                 // threads of a row in a group
+    static constexpr int kGroups = D == 128 ? 2 : 1;  // of row threads, taking blocks in turn
+    static_assert(kBufs % kGroups == 0, "a group waits for every use of its buffers");
+    static constexpr int kShare = D == 64 ? 4 : 2;    // threads of a row in a group
     static constexpr int kRowThreads = 128 * kGroups * kShare;
     static constexpr int kThreads = 32 * kCtrl + kRowThreads;
     // TMEM: buffer x: S at 128 x, dP at 128 x + 64 (P and dS over them); sums
@@ -152,6 +154,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             ptx::mbar_init(&sb->p_full[x], 128 * kShare);
             ptx::mbar_init(&sb->acc_done[x], 1);
         }
+        ptx::mbar_init(&sb->unit_done, 1);
         ptx::mbar_init(&sb->rest_full, C::kRowThreads);
         ptx::mbar_init(&sb->epi_done, C::kRowThreads);
         sb->abort = 0;
@@ -236,6 +239,7 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                         }
                     ptx::warp_mma_commit(&sb->acc_done[buf]);
                     ptx::warp_mma_commit(&sb->c_empty[stage]);
+                    if (b == x.nb - 1) ptx::warp_mma_commit(&sb->unit_done);
                 }
             }
             ptx::warp_mma_commit(&sb->drain[1]);
@@ -461,7 +465,9 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             }
             if (!ok) break;
             if (x.nb > 0) {
-                if (!warp_wait(&sb->acc_done[(i - 1) % NB], ((i - 1) / NB) & 1, &sb->abort, status)) break;
+                // (a barrier of the units: a group that has not seen the last but one use of the last block's buffer
+                // could not wait for the last by its parity)
+                if (!warp_wait(&sb->unit_done, use & 1, &sb->abort, status)) break;
                 ptx::tc_fence_after();
             }
             bool live = x.nb > 0;

@@ -102,6 +102,18 @@ def test_matches_the_definition(size, dtype, valid):
     check(f"{dtype} {valid} {size}", out, q, k, v, h, kv, ok, g)
 
 
+# many more units of work than SMs, groups that divide no tile, last tiles of one row, long states
+MANY = [(40, 600, 300, 4, 4, 32), (60, 300, 400, 2, 2, 64), (24, 400, 333, 6, 6, 128), (3, 200, 700, 6, 2, 64),
+        (2, 150, 300, 3, 1, 128), (1, 1100, 1300, 5, 1, 32), (2, 513, 2500, 2, 2, 32), (1, 129, 4097, 2, 2, 64),
+        (5, 1025, 257, 2, 1, 32), (70, 49, 100, 4, 4, 32), (9, 260, 256, 8, 2, 64)]
+
+
+@pytest.mark.parametrize("valid", ["all", "both"])
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_many_units_and_odd_groups(size, valid):
+    test_matches_the_definition(size, "bf16", valid)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_scores_and_scale(dtype):
     """A running maximum that keeps rising, sums dominated by one state, another scale."""

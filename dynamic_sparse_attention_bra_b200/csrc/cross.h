@@ -65,6 +65,10 @@ struct CrossParts {
     float2* ml;
 };
 
+// The scores of a call: what the forms of the kernels are chosen by, besides a
+// product's least size.
+inline long long cross_scores(const CrossGeom& g) { return (long long)g.rows * g.Lk * g.kv_heads * g.B; }
+
 // How a forward call is cut: by its sizes alone, so that the workspace's size
 // follows from the shape.
 struct CrossPlan {

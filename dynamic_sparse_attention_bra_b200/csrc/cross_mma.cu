@@ -367,18 +367,22 @@ int rows_per_cta(const CrossGeom& g, bool bf16) {
 // The states are split where (row tiles x state heads x entries) leave SMs
 // idle: enough parts for eight small CTAs on each SM (of which four run: entries
 // of different lengths even out; four parts: 81 us where eight take 76, sixteen
-// 82: 16 entries of up to 16384 states, 8 heads of 64), none below 256 states.
+// 82: 16 entries of up to 16384 states, 8 heads of 64), none below 256 states.  The
+// many-row form takes one CTA on an SM and parts of 128 states and more (2 x 4096 rows
+// of 64 over 1024 states: 17 us for 20 with parts of 512); at most 16, for the join
+// reads them all (128 rows of 32 over 8192: 20 us with 16 parts, 35 with 64); none
+// below 1024, where the parts' traffic costs more (64 x 256 rows of 128 over 512: 17 us
+// whole, 23 in two).
 CrossPlan cross_forward_plan(const CrossGeom& g, bool bf16) {
     CrossPlan p{1};
     const int sms = sm_count();
     if (sms <= 0 || g.Lk < 512) return p;
     const int rpc = rows_per_cta(g, bf16);
     const long long ctas = (long long)((g.rows + rpc - 1) / rpc) * g.kv_heads * g.B;
-    // the many-row form has one CTA of 256 rows on an SM; the others several small ones
     const bool tc = bf16 && cross_tc_covers(g);
     if (ctas <= 0 || ctas >= (tc ? 1LL : 2LL) * sms) return p;
     long long s = (tc ? 1LL : 8LL) * sms / ctas;
-    const long long most = g.Lk / (tc ? 512 : 256);
+    const long long most = tc ? (g.Lk < 1024 ? 1 : g.Lk < 2048 ? g.Lk / 128 : 16) : g.Lk / 256;
     if (s > most) s = most;
     p.splits = s < 1 ? 1 : (int)s;
     return p;

@@ -284,9 +284,12 @@ bra_status launch_d(const CrossGeom& g, const void* q, const void* k, const void
     const int sms = sm_count();
     if (sms <= 0) return BRA_ERR_CUDA;
     if (!allow_shared<bra_cross_short_kernel<D>>(kMaxStates * D * 4)) return BRA_ERR_CUDA;
-    // two CTAs an SM; fewer where the tiles do not give each warp one
-    const long long most = (long long)kCtas * sms, few = (tiles + kWarps - 1) / kWarps;
-    const int grid = (int)(few < most ? few : most);
+    // CTAs that keep to one (entry, state head), a tile a warp, where those fit on the
+    // SMs at once (32 entries of 32 rows over 64 states: 4 us; equal shares, which cross
+    // from one to the next and load twice, 11 us), else two an SM with equal shares
+    const long long most = (long long)kCtas * sms;
+    const long long whole = (long long)g.kv_heads * g.B * ((row_tiles + kWarps - 1) / kWarps);
+    const int grid = (int)(whole < most ? whole : most);
     const cudaError_t e = launch_after_previous(
         bra_cross_short_kernel<D>, dim3(grid), dim3(kThreads), bytes, stream, static_cast<const __nv_bfloat16*>(q),
         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse,
@@ -296,7 +299,16 @@ bra_status launch_d(const CrossGeom& g, const void* q, const void* k, const void
 
 }  // namespace
 
-bool cross_short_covers(const CrossGeom& g) { return g.rows > 16 && g.Lk <= kMaxStates && g.d <= 64; }
+// At d = 64 a small call is left to the streaming form, whose first tile of states is
+// there sooner (2 x 1024 rows over 256 states: 7.2 us for 8.9), a large one with more
+// than two of tcgen05's blocks to it (128 x 1024 rows over 192 states: 31 us for 34,
+// over 256: 33 for 43; over 128 26 where this form takes 26 too).
+bool cross_short_covers(const CrossGeom& g) {
+    if (g.rows <= 16 || g.Lk > kMaxStates || g.d > 64) return false;
+    if (g.d == 32) return true;
+    const long long scores = cross_scores(g);
+    return scores >= 1LL << 19 && (g.Lk <= 128 || scores < 1LL << 23);
+}
 
 bra_status cross_forward_short(const CrossGeom& g, const void* q, const void* k, const void* v, void* o, float* lse,
                                cudaStream_t stream) {

@@ -22,11 +22,14 @@
 // softmax ends.
 //
 // d = 32: a block costs a tile's threads its waits and TMEM latencies besides the
-// exponentials, so four tiles' share an SM: TILES_NOTE
+// exponentials, so four tiles share an SM (2 x 16,384 rows of 2 heads over 4096
+// states: 109 us for 132 with two tiles and blocks of 128).
 //
-// Bound by the exponentials (16 a clock and SM) for d = 32, by them and the
-// products for d = 128.  Every mbarrier wait is bounded; on expiry the kernel
-// records kDevTimeout, stops all roles, drains its products and frees TMEM.
+// Bound by the exponentials (16 a clock and SM) for d = 32, where they would take 61
+// of those 109 us, by them and the products for d = 128 (4 x 2048 tokens of 16 heads
+// on 4, up to 2048 states each: 106 us, 58 % of a large product's rate).
+// Every mbarrier wait is bounded; on expiry the kernel records kDevTimeout, stops
+// all roles, drains its products and frees TMEM.
 #include "cross_tc.cuh"
 #include "kernels.h"
 #include "tma_host.h"
@@ -517,7 +520,17 @@ bra_status launch_d(const CrossGeom& g, const TcPlan& plan, int grid, const void
 
 }  // namespace
 
-bool cross_tc_covers(const CrossGeom& g) { return g.rows >= 128; }
+// A full tile of rows, and enough work that a unit's start, end and waits are few of
+// its blocks and that units of 256 rows (512 at d = 32) fill the SMs; below, the
+// warps' form with its smaller units is ahead.  Its time and this form's, in us:
+//   d = 32   2 x 4096 rows x 1024 states (2^23 scores)  13 / 17, x 4096 (2^25)  57 / 38
+//   d = 64   16 x 256 rows x 512 (2^21)  13 / 15, 64 x 128 x 512 (2^22)  14 / 12,
+//            16 x 1024 x 512 (2^23)  20 / 15
+//   d = 128  16 x 256 x 320 (1.3 M)  11 / 13.5, 64 x 256 x 256 (2^22)  13.7 / 12.7,
+//            64 x 256 x 512 (2^23)  32 / 17
+bool cross_tc_covers(const CrossGeom& g) {
+    return g.rows >= 128 && cross_scores(g) >= (g.d == 32 ? 1LL << 24 : 1LL << 22);
+}
 
 int cross_tc_rows(const CrossGeom& g) { return 128 * (g.d == 32 ? Cfg<32>::kTiles : Cfg<64>::kTiles); }
 

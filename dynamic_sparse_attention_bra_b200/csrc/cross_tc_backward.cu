@@ -596,7 +596,19 @@ bra_status launch_d(const CrossGeom& g, int splits, const void* q, const void* k
 
 }  // namespace
 
-bool cross_tc_backward_covers(const CrossGeom& g) { return g.rows >= 128 && g.Lk >= 64; }
+// A full tile of rows, a full block of states, and enough work for the tiles of 128
+// to fill the SMs or, at d >= 64, to stream long enough; below, the warps' form with
+// tiles of 64 is ahead.  Forward and both gradients, its time and this form's, in us:
+//   d = 32   2 x 1024 rows x 1024 states (2^21 scores)  45 / 59, 64 x 192 x 256 (3 M)  26 / 30,
+//            64 x 512 x 128 (2^22)  32 / 28, 64 x 1024 x 256 (2^24)  80 / 59
+//   d = 64   2 x 128 x 128  19 / 21, 2 x 512 x 256  31 / 29, 2 x 128 x 4096 (2^20)  108 / 69,
+//            64 x 128 x 64 (2^19)  18 / 23, 64 x 128 x 128 (2^20)  22 / 23, 64 x 128 x 256  30 / 27
+//   d = 128  2 x 128 x 64  26 / 32, 2 x 128 x 256  38 / 36, 64 x 128 x 64 (2^19)  29 / 34,
+//            64 x 128 x 128 (2^20)  40 / 34
+bool cross_tc_backward_covers(const CrossGeom& g) {
+    if (g.rows < 128 || g.Lk < 64) return false;
+    return g.d == 32 ? cross_scores(g) >= 1LL << 22 : g.Lk >= 256 || cross_scores(g) >= 1LL << 20;
+}
 
 // Enough row splits for the tiles of states to fill the SMs, each of at least eight blocks of rows.
 int cross_tc_backward_splits(const CrossGeom& g) {

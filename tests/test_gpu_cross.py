@@ -106,6 +106,10 @@ def test_matches_the_definition(size, dtype, valid):
 MANY = [(40, 600, 300, 4, 4, 32), (60, 300, 400, 2, 2, 64), (24, 400, 333, 6, 6, 128), (3, 200, 700, 6, 2, 64),
         (2, 150, 300, 3, 1, 128), (1, 1100, 1300, 5, 1, 32), (2, 513, 2500, 2, 2, 32), (1, 129, 4097, 2, 2, 64),
         (5, 1025, 257, 2, 1, 32), (70, 49, 100, 4, 4, 32), (9, 260, 256, 8, 2, 64)]
+# as many scores as the many-row forms take, in units that end inside a tile; long splits
+MANY += [(3, 1030, 2900, 6, 2, 32), (1, 131, 33000, 4, 4, 32), (70, 129, 501, 4, 4, 32), (1, 4099, 1025, 4, 4, 32),
+         (3, 211, 1700, 6, 2, 64), (1, 129, 17001, 2, 2, 64), (9, 700, 256, 8, 2, 64), (40, 300, 90, 2, 2, 64),
+         (2, 450, 2300, 6, 2, 128), (1, 128, 33000, 1, 1, 128), (60, 129, 65, 9, 9, 128), (1, 2000, 513, 5, 5, 128)]
 
 
 @pytest.mark.parametrize("valid", ["all", "both"])
@@ -114,19 +118,20 @@ def test_many_units_and_odd_groups(size, valid):
     test_matches_the_definition(size, "bf16", valid)
 
 
+@pytest.mark.parametrize("Lq", [70, 9400])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_large_scores_and_scale(dtype):
+def test_large_scores_and_scale(dtype, Lq):
     """A running maximum that keeps rising, sums dominated by one state, another scale."""
-    B, Lq, Lk, h, d = 1, 70, 900, 2, 32
+    B, Lk, h, d = 1, 900, 2, 32
     q, g = tokens(1, B, Lq, h * d, dtype=T[dtype]), tokens(4, B, Lq, h * d, dtype=T[dtype])
     k, v = tokens(2, B, Lk, h * d, dtype=T[dtype]), tokens(3, B, Lk, h * d, dtype=T[dtype])
     k = (k.float() * torch.linspace(0.01, 12, Lk, device="cuda")[None, :, None]).to(T[dtype])
     ok = ref.valid_states(B, Lk, device="cuda")
-    check(f"rising {dtype}", run(q, k, v, h, h, grad=g, scale=0.3), q, k, v, h, h, ok, g, 0.3)
+    check(f"rising {dtype} {Lq}", run(q, k, v, h, h, grad=g, scale=0.3), q, k, v, h, h, ok, g, 0.3)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("Lq,heads", [(300, 4), (1, 4)])
+@pytest.mark.parametrize("Lq,heads", [(300, 4), (1, 4), (450, 4)])
 def test_slices_and_shared_states(dtype, Lq, heads):
     """K and V as halves of one projection, Q a slice of a wider tensor, states
     that all entries share (a batch step of 0): results as from dense copies."""
@@ -149,7 +154,7 @@ def test_offsets_past_32_bits():
     small = tokens(2, 2, 600, 128, dtype=torch.bfloat16)
     kv[0].copy_(small[0])
     kv[1].copy_(small[1])
-    for Lq in (1, 200):
+    for Lq in (1, 200, 1800):
         q, g = tokens(1, 2, Lq, 64, dtype=torch.bfloat16), tokens(3, 2, Lq, 64, dtype=torch.bfloat16)
         a = run(q, kv[..., :64], kv[..., 64:], 2, 2, grad=g)
         b = run(q, small[..., :64].contiguous(), small[..., 64:].contiguous(), 2, 2, grad=g)
@@ -178,7 +183,7 @@ def test_lengths_are_clamped():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("Lq,Lk", [(1, 6000), (400, 300)])
+@pytest.mark.parametrize("Lq,Lk", [(1, 6000), (400, 300), (2300, 2000)])
 def test_same_bits_again(dtype, Lq, Lk):
     q, g = tokens(1, 2, Lq, 128, dtype=T[dtype]), tokens(4, 2, Lq, 128, dtype=T[dtype])
     k, v = tokens(2, 2, Lk, 64, dtype=T[dtype]), tokens(3, 2, Lk, 64, dtype=T[dtype])

@@ -415,25 +415,35 @@ def bra_cross_attend_backward(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o,
 
 
 def bra_cross_device_status(shape: BraCrossShape, workspace, stream=None) -> int:
-    """Synchronises the stream; returns (and clears) the device status code."""
-    return int(_lib.bra_cross_device_status(ctypes.byref(shape), _ptr(workspace), _stream(stream)))
+    """Synchronises the stream (None: the workspace's device's current one);
+    returns (and clears) the device status code."""
+    import torch
+    dev = _cuda_device(workspace, "cross attention")
+    raw = _current_stream(dev) if stream is None else _stream(stream)
+    with torch.cuda.device(dev):
+        return int(_lib.bra_cross_device_status(ctypes.byref(shape), _ptr(workspace), raw))
 
 
 def cross_attention(q, k, v, heads: int, kv_heads: int | None = None, kv_len=None, kv_mask=None,
                     scale: float | None = None, stream=None):
     """(o, lse) of q [B, Lq, heads * d] over the states k, v [B, Lk, kv_heads * d].
 
-    Allocates o, lse and a zeroed workspace with torch on q's device, then runs
-    ``bra_cross_attend``."""
+    Allocates o, lse and a zeroed workspace with torch on q's device (as
+    ``stream``'s, where one is given: what is freed is not used again before the
+    kernels end), then runs ``bra_cross_attend``."""
     import torch
     shape = cross_shape_for(q, k, v, heads, kv_heads, scale)
     nbytes = bra_cross_workspace_bytes(shape)
     if nbytes == 0:
         raise BraError(BRA_ERR_INVALID_ARG if shape.d in (32, 64, 128) else BRA_ERR_UNSUPPORTED, "cross_attention")
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((shape.B, heads, shape.Lq), dtype=torch.float32, device=q.device)
-    bra_cross_attend(shape, q, k, v, kv_len, kv_mask, o, lse, ws, stream)
+    _cuda_device(q, "cross attention")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=q.device)
+    with torch.cuda.stream(stream):  # None: as it is
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty((shape.B, heads, shape.Lq), dtype=torch.float32, device=q.device)
+        bra_cross_attend(shape, q, k, v, kv_len, kv_mask, o, lse, ws, stream)
     return o, lse
 
 

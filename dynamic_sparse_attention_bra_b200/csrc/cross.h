@@ -67,7 +67,7 @@ struct CrossParts {
 
 // The scores of a call: what the forms of the kernels are chosen by, besides a
 // product's least size.
-inline long long cross_scores(const CrossGeom& g) { return (long long)g.rows * g.Lk * g.kv_heads * g.B; }
+inline double cross_scores(const CrossGeom& g) { return (double)g.rows * g.Lk * g.kv_heads * g.B; }
 
 // How a forward call is cut: by its sizes alone, so that the workspace's size
 // follows from the shape.

@@ -373,6 +373,10 @@ bra_cross_dkv_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* _
     for (int h = 0; h < 2; ++h) {
         const int key = kt * 64 + warp * 16 + h * 8 + (lane >> 2);
         if (key >= g.Lk) continue;
+        if (!on[h]) {  // an infinite gradient times its P of zero has made these sums NaN
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) ak[i][2 * h] = ak[i][2 * h + 1] = av[i][2 * h] = av[i][2 * h + 1] = 0.f;
+        }
         const size_t at = (((size_t)b * g.Lk + key) * g.kv_heads + j) * D + (lane & 3) * 2;
         if (splits > 1) {
             float* pk = parts + (size_t)split * 2 * elems + at;

@@ -306,7 +306,7 @@ bra_status launch_d(const CrossGeom& g, const void* q, const void* k, const void
 bool cross_short_covers(const CrossGeom& g) {
     if (g.rows <= 16 || g.Lk > kMaxStates || g.d > 64) return false;
     if (g.d == 32) return true;
-    const long long scores = cross_scores(g);
+    const double scores = cross_scores(g);
     return scores >= 1LL << 19 && (g.Lk <= 128 || scores < 1LL << 23);
 }
 

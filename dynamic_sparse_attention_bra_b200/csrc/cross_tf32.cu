@@ -656,6 +656,10 @@ bra_cross_tf32_dkv_kernel(const float* __restrict__ q, const float* __restrict__
     for (int h = 0; h < 2; ++h) {
         const int key = kt * 64 + pair * 16 + h * 8 + gq;
         if (key >= g.Lk) continue;
+        if (!on[h]) {  // an infinite gradient times its P of zero has made these sums NaN
+#pragma unroll
+            for (int i = 0; i < 4 * G::kBlocks; ++i) ak[i][2 * h] = ak[i][2 * h + 1] = av[i][2 * h] = av[i][2 * h + 1] = 0.f;
+        }
         const size_t at = (((size_t)b * g.Lk + key) * g.kv_heads + j) * D + half * G::kBlocks * 32;
         store_row(ok + at, ak, h, g.scale, t4);
         store_row(ov + at, av, h, 1.f, t4);

@@ -292,6 +292,7 @@ bra_status bra_selftest_bounded_wait(const bra_shape* shape, void* workspace, un
  * asynchrony, alignment (16 bytes) and errors are as above: an invalid call
  * returns an error and launches nothing, and nothing is allocated.  All
  * buffers and the stream belong to the calling thread's current device.
+ * Outputs overlap neither inputs nor each other unless a call says so.
  */
 
 /*
@@ -391,10 +392,12 @@ typedef struct {
 /*
  * Pair i turns by pos[axis(i)] * inv_freq[i] radians:
  *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
- * the angle formed and reduced in fp64, the rotation in fp32, rounded once.
+ * the angle formed as a 64-bit fraction of a turn and reduced modulo a turn,
+ * within 2^-31 of a turn at any 32-bit position; the rotation in fp32, rounded once.
  *   pos       device int32 [B or 1, L, 3] (time, height, width of each token),
  *             or NULL: token l = (t * H + y) * W + x is at (t, y, x)
- *   inv_freq  device fp32 [P]: one frequency for each pair (any base or layout)
+ *   inv_freq  device fp32 [P]: one frequency for each pair (any base or layout),
+ *             finite and below 2^50 in magnitude
  *   q_out, k_out  written; either may be its input (with equal strides), other
  *             overlaps are not allowed
  * K is optional: k = k_out = NULL.

@@ -272,3 +272,46 @@ def test_wrapper_on_a_map():
         bra.cross_attention(q, k, k, 8)  # d = 16
     with pytest.raises(ValueError):
         bra.cross_attention(q, k.cpu(), k, 4)
+
+
+# one size for every form of the kernels, forward and backward
+FORMS = [(2, 3, 600, 4, 2, 32), (2, 40, 300, 4, 2, 128), (3, 200, 77, 2, 2, 32), (40, 250, 100, 2, 2, 64),
+         (20, 600, 400, 4, 4, 32), (6, 513, 700, 4, 2, 64), (3, 600, 900, 4, 4, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+def test_a_token_that_is_not_finite_stays_with_its_own(size, dtype):
+    """NaN in one token's Q and infinities in its gradient: the other tokens' o, lse and dq, and
+    all of the other entries' gradients, keep their bits; invalid states still get zeros."""
+    B, Lq, Lk, h, kv, d = size
+    t = T[dtype]
+    q, g = tokens(1, B, Lq, h * d, dtype=t), tokens(4, B, Lq, h * d, dtype=t)
+    k, v = tokens(2, B, Lk, kv * d, dtype=t), tokens(3, B, Lk, kv * d, dtype=t)
+    m = (torch.rand((B, Lk), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda") < 0.7).to(torch.uint8)
+    n = torch.full((B,), Lk - 1, dtype=torch.int32, device="cuda")
+    ok = ref.valid_states(B, Lk, n, m, "cuda")
+    a = run(q, k, v, h, kv, n, m, g)
+    q2, g2 = q.clone(), g.clone()
+    q2[1, Lq // 2, 5], g2[1, Lq // 2] = float("nan"), float("inf")
+    b = run(q2, k, v, h, kv, n, m, g2)
+    others = torch.ones((B, Lq), dtype=torch.bool, device="cuda")
+    others[1, Lq // 2] = False
+    for x in ("o", "dq"):
+        assert torch.equal(a[x][others], b[x][others]), x
+    assert torch.equal(a["lse"].transpose(1, 2)[others], b["lse"].transpose(1, 2)[others])
+    for x in ("dk", "dv"):
+        assert torch.equal(a[x][0], b[x][0]) and torch.equal(a[x][2:], b[x][2:]), x
+        assert float(b[x][~ok].float().abs().max()) == 0, x
+
+
+def test_a_stream_s_memory_is_its_own():
+    """The wrapper's workspace, freed as it returns, is not handed out again under its kernels."""
+    q, k = tokens(1, 2, 300, 256, dtype=torch.bfloat16), tokens(2, 2, 6000, 256, dtype=torch.bfloat16)
+    o, lse = bra.cross_attention(q, k, k, 8)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        o2, lse2 = bra.cross_attention(q, k, k, 8, stream=stream)
+        junk = [torch.full((1 << 21,), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and len(junk) == 8

@@ -499,7 +499,7 @@ bra_cross_tf32_dq_kernel(const float* __restrict__ q, const float* __restrict__ 
             for (int i = 0; i < 4; ++i) {
                 const bool on = (w >> (i * 8 + t4 * 2 + (e & 1))) & 1u;
                 const float p = on ? ptx::ex2(fmaf(s[i][e], c2, -off)) : 0.f;
-                s[i][e] = p * (dp[i][e] - dd);
+                s[i][e] = on ? p * (dp[i][e] - dd) : 0.f;  // (an infinite dO makes NaN of dP)
                 dp[i][e] = p;
                 rest[e >> 1] += s[i][e];
             }

@@ -315,3 +315,19 @@ def test_a_stream_s_memory_is_its_own():
         junk = [torch.full((1 << 21,), float("nan"), device="cuda") for _ in range(8)]
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(lse, lse2) and len(junk) == 8
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+def test_an_entry_without_states_gets_zeros_from_any_gradient(size, dtype):
+    B, Lq, Lk, h, kv, d = size
+    t = T[dtype]
+    q, g = tokens(1, B, Lq, h * d, dtype=t), tokens(4, B, Lq, h * d, dtype=t)
+    k, v = tokens(2, B, Lk, kv * d, dtype=t), tokens(3, B, Lk, kv * d, dtype=t)
+    m = torch.ones((B, Lk), dtype=torch.bool, device="cuda")
+    m[0] = False
+    g[0, Lq // 2], g[0, 0, 1] = float("inf"), float("nan")
+    out = run(q, k, v, h, kv, None, m, g)
+    assert bool((out["lse"][0] == -math.inf).all())
+    assert all(float(out[x][0].float().abs().max()) == 0 for x in ("o", "dq", "dk", "dv"))
+    assert all(bool(torch.isfinite(out[x][1:]).all()) for x in out)

@@ -331,3 +331,42 @@ def test_an_entry_without_states_gets_zeros_from_any_gradient(size, dtype):
     assert bool((out["lse"][0] == -math.inf).all())
     assert all(float(out[x][0].float().abs().max()) == 0 for x in ("o", "dq", "dk", "dv"))
     assert all(bool(torch.isfinite(out[x][1:]).all()) for x in out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("spans", ["left", "hole", "last"])
+def test_masks_of_whole_blocks(size, dtype, spans):
+    """Padding on the left, invalid stretches longer than any block, one valid state at the very end."""
+    B, Lq, Lk, h, kv, d = size
+    t = T[dtype]
+    q, g = tokens(1, B, Lq, h * d, dtype=t), tokens(4, B, Lq, h * d, dtype=t)
+    k, v = tokens(2, B, Lk, kv * d, dtype=t, mean=0.5), tokens(3, B, Lk, kv * d, dtype=t, mean=0.3)
+    m = torch.zeros((B, Lk), dtype=torch.uint8, device="cuda")
+    for b in range(B):
+        if spans == "left":
+            m[b, min(Lk - 1, (b + 1) * Lk // (B + 1)):] = 1
+        elif spans == "hole":
+            m[b, : 1 + b % 3] = 1
+            m[b, Lk - 1 - b % 5:] = 1
+        else:
+            m[b, -1] = 1
+    ok = ref.valid_states(B, Lk, None, m, "cuda")
+    k2, v2 = (torch.where(ok[:, :, None], x, float("nan")) for x in (k, v))
+    check(f"spans {spans} {dtype} {size}", run(q, k2, v2, h, kv, None, m, g), q, k, v, h, kv, ok, g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+def test_scores_far_from_zero(size, dtype):
+    """Scores around +-3000: the first states far below the last, and all of them far below zero."""
+    B, Lq, Lk, h, kv, d = size
+    t = T[dtype]
+    k, v = torch.ones((B, Lk, kv * d), device="cuda"), tokens(3, B, Lk, kv * d, dtype=t)
+    k = (k * torch.linspace(-30, 30, Lk, device="cuda")[None, :, None]).to(t)
+    for sign in (1.0, -1.0):
+        q = torch.full((B, Lq, h * d), sign * 100 / d, device="cuda").to(t)
+        out = run(q, k, v, h, kv, scale=1.0)
+        check(f"far {dtype} {size} {sign}", out, q, k, v, h, kv, ref.valid_states(B, Lk, device="cuda"), None, 1.0)
+        out = run(q, (k.float() - 30.5 * sign).to(t), v, h, kv, scale=1.0)
+        assert bool(torch.isfinite(out["o"]).all()) and float(out["lse"].max()) < 0

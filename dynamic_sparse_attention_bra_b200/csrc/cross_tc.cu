@@ -30,6 +30,7 @@
 // on 4, up to 2048 states each: 106 us, 58 % of a large product's rate).
 // Every mbarrier wait is bounded; on expiry the kernel records kDevTimeout, stops
 // all roles, drains its products and frees TMEM.
+#include "cross_map.h"
 #include "cross_tc.cuh"
 #include "kernels.h"
 #include "tma_host.h"

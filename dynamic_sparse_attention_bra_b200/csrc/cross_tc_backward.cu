@@ -29,6 +29,7 @@
 // tiles, of which a row's threads waited 2360.
 // Every mbarrier wait is bounded; on expiry the kernel records kDevTimeout, stops
 // all roles, drains its products and frees TMEM.
+#include "cross_map.h"
 #include "cross_tc.cuh"
 #include "kernels.h"
 #include "tma_host.h"

@@ -4,7 +4,7 @@
 #pragma once
 
 #include "cross.h"
-#include "tc_ptx.cuh"
+#include "cross_ptx.cuh"
 #include "warp_mma.cuh"
 
 namespace bra {

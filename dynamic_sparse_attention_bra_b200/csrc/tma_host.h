@@ -26,13 +26,6 @@ bool encode_region_major_map(CUtensorMap* map, const void* base, int B, int H, i
 // boxes reaching past the map are zero-filled.
 bool encode_halo_map(CUtensorMap* map, const void* base, int B, int H, int W, int C, int box_w, int box_h);
 
-// Tensor map of [B, L, heads, d] bf16 tokens with steps of ``row`` and ``batch``
-// elements, whose box is box_tokens tokens of box_heads heads, 32 channels
-// (64-byte swizzle) or 64 (128-byte swizzle) of each, landing as box_tokens x
-// box_heads rows.  False too where a step does not fit a tensor map.
-bool encode_heads_map(CUtensorMap* map, const void* base, int B, int L, int heads, int d, long long row,
-                      long long batch, int box_tokens, int box_heads);
-
 // Number of SMs of the current device (cached per device).
 int sm_count();
 

@@ -121,14 +121,19 @@ __device__ __forceinline__ void attend(Tile<D>& x, uint32_t k_lane, uint32_t k_n
         x.mx[h] = mn;
     }
     const float n0 = x.mx[0] == -INFINITY ? 0.f : -x.mx[0], n1 = x.mx[1] == -INFINITY ? 0.f : -x.mx[1];
+    const uint64_t sl2 = ptx::pack_f32x2(sl, sl), n02 = ptx::pack_f32x2(n0, n0), n12 = ptx::pack_f32x2(n1, n1);
+    uint64_t sums[2] = {ptx::pack_f32x2(x.sum[0], 0.f), ptx::pack_f32x2(x.sum[1], 0.f)};
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         uint32_t pa[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {  // tile 2 i + y / 2, row gq or gq + 8
             const float* sc = s[2 * i + (y >> 1)] + 2 * (y & 1);
-            const float lo = ptx::ex2(fmaf(sc[0], sl, y & 1 ? n1 : n0)), hi = ptx::ex2(fmaf(sc[1], sl, y & 1 ? n1 : n0));
-            x.sum[y & 1] += lo + hi;
+            float lo, hi;
+            ptx::unpack_f32x2(ptx::fma_f32x2(ptx::pack_f32x2(sc[0], sc[1]), sl2, y & 1 ? n12 : n02), lo, hi);
+            lo = ptx::ex2(lo);
+            hi = ptx::ex2(hi);
+            sums[y & 1] = ptx::add_f32x2(sums[y & 1], ptx::pack_f32x2(lo, hi));
             pa[y] = ptx::pack_bf16x2(lo, hi);
         }
 #pragma unroll
@@ -143,6 +148,12 @@ __device__ __forceinline__ void attend(Tile<D>& x, uint32_t k_lane, uint32_t k_n
                 mma16816(x.acc[c + 1], pa[0], pa[1], pa[2], pa[3], bf[2], bf[3]);
             }
         }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float lo, hi;
+        ptx::unpack_f32x2(sums[h], lo, hi);
+        x.sum[h] = lo + hi;
     }
 }
 

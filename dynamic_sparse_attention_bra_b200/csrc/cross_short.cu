@@ -14,8 +14,9 @@
 // does not mind), as one 16-byte shared load for two products.  The next tile's Q
 // is loaded under this tile's products; O leaves in 16-byte stores after a 4 x 4
 // exchange in the quad.
-// Bound by its instructions, about 600 for 16 rows and 64 states, and the first
-// loads: 200,704 x 2 rows over 77 states (lengths from 39 on) take 32 us, of which
+// Bound by the latency of a warp's chain (about 550 instructions for 16 rows and 64
+// states, half of the issue slots) and the first loads: 200,704 x 2 rows over 77 states
+// (lengths from 39 on) take 32 us, of which
 // memory would take 8; the tcgen05 form takes 51-61 us there, its roles' hand-over
 // costing more than the work of one short block.
 #include "cross_tile.cuh"
@@ -32,7 +33,7 @@ using wmma16::mma16816_first;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxStates = 256;
-constexpr int kCtas = 2;  // on an SM (three of 80 registers a thread: 34.6 us for 32.4)
+constexpr int kCtas = 2;  // on an SM (three of 80 registers a thread: 34.7 us for 31.7)
 
 // K is read as 16-byte chunks by quads: at 128-byte rows, odd rows swap their halves.
 template <int D>
@@ -313,7 +314,7 @@ bra_status launch_d(const CrossGeom& g, const void* q, const void* k, const void
 // At d = 64 a small call is left to the streaming form, whose first tile of states is
 // there sooner (2 x 1024 rows over 256 states: 7.2 us for 8.9), a large one with more
 // than two of tcgen05's blocks to it (128 x 1024 rows over 192 states: 31 us for 34,
-// over 256: 33 for 43; over 128 26 where this form takes 26 too).
+// over 256: 33 for 43; over 128 both take 26).
 bool cross_short_covers(const CrossGeom& g) {
     if (g.rows <= 16 || g.Lk > kMaxStates || g.d > 64) return false;
     if (g.d == 32) return true;

@@ -39,36 +39,14 @@ Divisor divisor(int d) { return {(uint32_t)d, d > 1 ? (uint32_t)((1ull << 32) / 
 // halves and their V partners P channels on (split halves), or V channels
 // past 2 P that are copied.
 template <typename T, int V>
-struct Vec {
-    using type = uint4;
-};
-template <>
-struct Vec<__nv_bfloat16, 1> {
-    using type = __nv_bfloat16;
-};
-template <>
-struct Vec<float, 1> {
-    using type = float;
-};
-
-template <typename T, int V>
-__device__ __forceinline__ void widen(const typename Vec<T, V>::type& x, float (&f)[V]) {
-    if constexpr (V == 1) f[0] = to_f32(x);
-    else unpack16(x, f, static_cast<const T*>(nullptr));
-}
-template <typename T, int V>
-__device__ __forceinline__ typename Vec<T, V>::type narrow(const float (&f)[V]) {
-    if constexpr (V == 1) {
-        return from_f32<T>(f[0]);
-    } else if constexpr (V == 4) {
+__device__ __forceinline__ uint4 narrow(const float (&f)[V]) {
+    if constexpr (V == 4) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     } else {
-        uint4 u;
         __nv_bfloat162 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        u = *reinterpret_cast<uint4*>(h);
-        return u;
+        return *reinterpret_cast<uint4*>(h);
     }
 }
 
@@ -86,8 +64,8 @@ template <typename T, int V, bool PAIRED>
 __global__ void __launch_bounds__(kThreads, 3)
 bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_freq, T* qo, T* ko, RotaryGeom g,
                   int tokens_per_cta, int units_turn, Divisor units) {
-    using U = typename Vec<T, V>::type;
-    constexpr int A = PAIRED ? V : (V > 1 ? V / 2 : 1);  // pairs of a unit
+    using U = uint4;
+    constexpr int A = PAIRED ? V : V / 2;  // pairs of a unit
     __shared__ uint64_t turns[kMaxPairs];
     // CTA = consecutive tokens of one entry
     const int b = blockIdx.y, l0 = blockIdx.x * tokens_per_cta, here = min(tokens_per_cta, g.L - l0);
@@ -155,8 +133,8 @@ bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_f
                     *reinterpret_cast<U*>(d) = va[i];
                 } else if constexpr (PAIRED) {
                     float f[V], z[V];
-                    widen<T, V>(va[i], f);
-                    widen<T, V>(vz[i], z);
+                    unpack16(va[i], f, static_cast<const T*>(nullptr));
+                    unpack16(vz[i], z, static_cast<const T*>(nullptr));
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float w = f[e] * cs[e] - z[e] * sn[e];
@@ -167,7 +145,7 @@ bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_f
                     *reinterpret_cast<U*>(d + g.P) = narrow<T, V>(z);
                 } else {
                     float f[V];
-                    widen<T, V>(va[i], f);
+                    unpack16(va[i], f, static_cast<const T*>(nullptr));
 #pragma unroll
                     for (int e = 0; e < V; e += 2) {
                         if ((c + e) / 2 >= g.P) break;
@@ -181,6 +159,113 @@ bra_rotary_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_f
         }
     }
     allow_dependents();
+}
+
+// Split halves of which P channels are no whole vectors: a pair's channels lie at
+// different places of two vectors.  A thread has one vector of a token in all heads;
+// the rows go through shared memory, where it reads its channels' partners, and the
+// CTA's sines are a table there.  (64 x 56 x 56 tokens, 2 + 2 heads of 32 in bf16, 15
+// pairs: 44 us; two-byte loads and stores of whole pairs 57.)
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 4)
+bra_rotary_split_kernel(const T* q, const T* k, const int32_t* pos, const float* inv_freq, T* qo, T* ko, RotaryGeom g,
+                        int tokens_per_cta, int tokens_per_pass, Divisor units, Divisor pairs) {
+    __shared__ uint64_t turns[kMaxPairs];
+    __shared__ float2 table[kThreads * V / 2];  // (cosine, sine) [token][pair]
+    __shared__ __align__(16) T rows[kThreads * kHeads * V];  // [token][head][channel]
+    const int b = blockIdx.y, l0 = blockIdx.x * tokens_per_cta, l1 = min(l0 + tokens_per_cta, g.L);
+    const int tk = divide(threadIdx.x, units), c = ((int)threadIdx.x - tk * (int)units.d) * V;
+    const int all = g.heads + g.kv_heads;
+    grid_dependency_wait();
+    for (int i = threadIdx.x; i < g.P; i += kThreads) {
+        const uint64_t f = turns_of(__ldcg(inv_freq + i));
+        turns[i] = g.inverse ? 0ull - f : f;
+    }
+    for (int first = l0; first < l1; first += tokens_per_pass) {
+        const int here = min(tokens_per_pass, l1 - first), l = first + tk;
+        const bool in = tk < here;
+        const size_t in_q = (size_t)b * g.q_batch + (size_t)l * g.q_row + c, in_k = (size_t)b * g.k_batch + (size_t)l * g.k_row + c;
+        const size_t out_q = (size_t)b * g.qo_batch + (size_t)l * g.qo_row + c,
+                     out_k = (size_t)b * g.ko_batch + (size_t)l * g.ko_row + c;
+        uint4 va[kHeads];
+        auto fetch = [&](int h) {
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int y = h + i;
+                if (in && y < all)
+                    va[i] = *reinterpret_cast<const uint4*>(y < g.heads ? q + in_q + y * g.d : k + in_k + (y - g.heads) * g.d);
+            }
+        };
+        fetch(0);
+        __syncthreads();  // the frequencies are there; the last pass's table and rows are read
+        for (int e = threadIdx.x; e < here * g.P; e += kThreads) {
+            const int t = divide(e, pairs), i = e - t * g.P, at = first + t;
+            int p;
+            if (pos) {
+                p = __ldcg(pos + (size_t)b * g.pos_batch + (size_t)at * 3 + (i < g.axis1 ? 0 : (i < g.axis2 ? 1 : 2)));
+            } else {
+                const int row = at / g.W, time = row / g.H;
+                p = i < g.axis1 ? time : (i < g.axis2 ? row - time * g.H : at - row * g.W);
+            }
+            const int angle = (int)(((uint64_t)(int64_t)p * turns[i]) >> 32);
+            float2 v;
+            sincospif((float)angle * 4.656612873077393e-10f, &v.y, &v.x);
+            table[e] = v;
+        }
+        float2 turn[V];  // (cosine, +- sine) of this thread's channels
+        for (int h = 0; h < all; h += kHeads) {
+            if (h > 0) {
+                fetch(h);
+                __syncthreads();  // the last heads' rows are read
+            }
+            T* mine = rows + (size_t)tk * kHeads * g.d + c;
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i)
+                if (in && h + i < all) *reinterpret_cast<uint4*>(mine + i * g.d) = va[i];
+            __syncthreads();
+            if (!in) continue;
+            if (h == 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const int j = c + e;
+                    turn[e] = j >= 2 * g.P ? make_float2(1.f, 0.f) : table[tk * g.P + (j < g.P ? j : j - g.P)];
+                    if (j < g.P) turn[e].y = -turn[e].y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                const int y = h + i;
+                if (y >= all) break;
+                float f[V], z[V];
+                unpack16(va[i], f, static_cast<const T*>(nullptr));
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const int j = c + e;
+                    z[e] = to_f32(mine[i * g.d + e + (j < g.P ? g.P : j < 2 * g.P ? -g.P : 0)]);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (c + e < 2 * g.P) f[e] = f[e] * turn[e].x + z[e] * turn[e].y;
+                *reinterpret_cast<uint4*>(y < g.heads ? qo + out_q + y * g.d : ko + out_k + (y - g.heads) * g.d) =
+                    narrow<T, V>(f);
+            }
+        }
+    }
+    allow_dependents();
+}
+
+template <typename T, int V>
+cudaError_t launch_split(const RotaryGeom& g, const void* q, const void* k, const int32_t* pos, const float* inv_freq,
+                         void* q_out, void* k_out, cudaStream_t stream) {
+    const int units = g.d / V, pass = kThreads / units;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // two passes a CTA where that still gives each SM four CTAs
+    const int per = (long long)g.B * g.L * units > 8LL * kThreads * sms ? 2 * pass : pass;
+    return launch_after_previous(bra_rotary_split_kernel<T, V>, dim3((unsigned)((g.L + per - 1) / per), (unsigned)g.B),
+                                 dim3(kThreads), 0, stream, static_cast<const T*>(q), static_cast<const T*>(k), pos,
+                                 inv_freq, static_cast<T*>(q_out), static_cast<T*>(k_out), g, per, pass,
+                                 divisor(units), divisor(g.P));
 }
 
 template <typename T, int V, bool PAIRED>
@@ -207,7 +292,7 @@ bra_status rotary_launch(const RotaryGeom& g, bool bf16, const void* q, const vo
                          const float* inv_freq, void* q_out, void* k_out, cudaStream_t stream) {
     const int v = bf16 ? 8 : 4;
     cudaError_t e;
-    // split halves whose P channels are whole vectors move 16 bytes at a time, others one channel
+    // split halves whose P channels are whole vectors pair them in a thread's registers
     const bool wide = g.P % v == 0;
     if (g.interleaved)
         e = bf16 ? launch<__nv_bfloat16, 8, false>(g, q, k, pos, inv_freq, q_out, k_out, stream)
@@ -216,8 +301,8 @@ bra_status rotary_launch(const RotaryGeom& g, bool bf16, const void* q, const vo
         e = bf16 ? launch<__nv_bfloat16, 8, true>(g, q, k, pos, inv_freq, q_out, k_out, stream)
                  : launch<float, 4, true>(g, q, k, pos, inv_freq, q_out, k_out, stream);
     else
-        e = bf16 ? launch<__nv_bfloat16, 1, true>(g, q, k, pos, inv_freq, q_out, k_out, stream)
-                 : launch<float, 1, true>(g, q, k, pos, inv_freq, q_out, k_out, stream);
+        e = bf16 ? launch_split<__nv_bfloat16, 8>(g, q, k, pos, inv_freq, q_out, k_out, stream)
+                 : launch_split<float, 4>(g, q, k, pos, inv_freq, q_out, k_out, stream);
     return e == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
 }
 

@@ -35,6 +35,12 @@ ROTARY = [
 ]
 
 
+# pairs that are no whole vectors: many heads, vectors that hold both halves' ends, head sizes that divide no
+# CTA, more than one pass
+ROTARY += [(2, (2, 13, 17), 6, 3, 24, (3, 2, 4)), (1, (1, 40, 9), 5, 5, 40, (5, 5, 5)), (3, (4, 7, 9), 9, 1, 64, (13, 9, 9)),
+           (1, (1, 3, 2), 2, 1, 512, (100, 100, 51)), (40, (1, 56, 56), 2, 2, 32, (5, 5, 5)), (2, (1, 5, 7), 1, 1, 32, (1, 0, 0))]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "interleaved"])
 @pytest.mark.parametrize("case", ROTARY, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}x{c[4]}")
@@ -72,9 +78,10 @@ def test_rotary_far_positions():
     assert float((out.double() - want).abs().max()) <= float(q.abs().max()) * (2.0 ** -18 + 2.0 ** -20)
 
 
+@pytest.mark.parametrize("pairs", [(0, 8, 8), (0, 7, 6)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_rotary_in_place_slices_and_inverse(dtype):
-    t, pairs, f = T[dtype], (0, 8, 8), freqs((0, 8, 8))
+def test_rotary_in_place_slices_and_inverse(dtype, pairs):
+    t, f = T[dtype], freqs(pairs)
     wide = tokens(1, 2, 49, 3 * 64, dtype=t)  # a projection's q | k | v
     keep = wide.clone()
     q, k = wide[..., :64], wide[..., 64:128]

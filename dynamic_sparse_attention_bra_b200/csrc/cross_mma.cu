@@ -255,13 +255,13 @@ bra_cross_mma_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* _
                 *reinterpret_cast<float4*>(parts.o + at * D + c) = x;
                 if (c == 0) parts.ml[at] = make_float2(mm, ll);
             } else {
-                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                const float inv = inverse_sum(ll);
                 uint2 w;
                 w.x = ptx::pack_bf16x2(x.x * inv, x.y * inv);
                 w.y = ptx::pack_bf16x2(x.z * inv, x.w * inv);
                 *reinterpret_cast<uint2*>(o + cross_o_offset(g, b, j, row0 + r) + c) = w;
                 if (c == 0 && lse)
-                    lse[cross_lse_offset(g, b, j, row0 + r)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                    lse[cross_lse_offset(g, b, j, row0 + r)] = log_sum(mm, ll);
             }
         }
     } else {
@@ -280,14 +280,14 @@ bra_cross_mma_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* _
                             make_float2(acc[mi][i][2 * h], acc[mi][i][2 * h + 1]);
                     if ((lane & 3) == 0) parts.ml[at] = make_float2(m[mi][h], ll);
                 } else {
-                    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                    const float inv = inverse_sum(ll);
                     __nv_bfloat16* row = o + cross_o_offset(g, b, j, r) + (lane & 3) * 2;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
                         *reinterpret_cast<uint32_t*>(row + i * 8) =
                             ptx::pack_bf16x2(acc[mi][i][2 * h] * inv, acc[mi][i][2 * h + 1] * inv);
                     if ((lane & 3) == 0 && lse)
-                        lse[cross_lse_offset(g, b, j, r)] = ll > 0.f ? (m[mi][h] + log2f(ll)) * kLn2 : -INFINITY;
+                        lse[cross_lse_offset(g, b, j, r)] = log_sum(m[mi][h], ll);
                 }
             }
     }
@@ -323,13 +323,13 @@ bra_cross_join_kernel(CrossParts parts, T* __restrict__ o, float* __restrict__ l
     const int r = (int)(at % g.rows);
     const long long bj = at / g.rows;
     const int j = (int)(bj % g.kv_heads), b = (int)(bj / g.kv_heads);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
     T* row = o + cross_o_offset(g, b, j, r) + c;
     row[0] = from_f32<T>(x.x * inv);
     row[1] = from_f32<T>(x.y * inv);
     row[2] = from_f32<T>(x.z * inv);
     row[3] = from_f32<T>(x.w * inv);
-    if (c == 0 && lse) lse[cross_lse_offset(g, b, j, r)] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (c == 0 && lse) lse[cross_lse_offset(g, b, j, r)] = log_sum(m, l);
 }
 
 template <int D, int WM, int WN, int MI>

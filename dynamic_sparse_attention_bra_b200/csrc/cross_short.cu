@@ -263,7 +263,7 @@ bra_cross_short_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16*
                 x.sum[h] += __shfl_xor_sync(0xffffffffu, x.sum[h], 1);
                 x.sum[h] += __shfl_xor_sync(0xffffffffu, x.sum[h], 2);
                 const int r = tile * 16 + h * 8 + gq;
-                const float inv = x.sum[h] > 0.f ? 1.f / x.sum[h] : 0.f;
+                const float inv = inverse_sum(x.sum[h]);
                 int t = r, hh = 0;
                 if (g.rep > 1) {
                     t = r / g.rep;
@@ -280,7 +280,7 @@ bra_cross_short_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16*
                     if (r < g.rows) dst[4 * m] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (lse && t4 == 0 && r < g.rows)
-                    lse[((size_t)b * g.heads + (size_t)(j * g.rep + hh)) * g.Lq + t] = x.sum[h] > 0.f ? (x.mx[h] + log2f(x.sum[h])) * kLn2 : -INFINITY;
+                    lse[((size_t)b * g.heads + (size_t)(j * g.rep + hh)) * g.Lq + t] = log_sum(x.mx[h], x.sum[h]);
             }
         }
     }

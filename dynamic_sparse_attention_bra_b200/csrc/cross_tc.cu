@@ -456,7 +456,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const float l = lo + hi;
             const int r0 = x.row0 + tile * 128 + row;
             const bool in = r0 < g.rows;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = inverse_sum(l);
             const size_t part = ((size_t)(x.split * g.B + x.b) * g.kv_heads + x.j) * g.rows + r0;
             __nv_bfloat16* orow = in ? o + cross_o_offset(g, x.b, x.j, r0) : o;
 #pragma unroll 1
@@ -485,7 +485,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             }
             if (in) {
                 if (p.splits > 1) parts.ml[part] = make_float2(m, l);
-                else if (lse) lse[cross_lse_offset(g, x.b, x.j, r0)] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                else if (lse) lse[cross_lse_offset(g, x.b, x.j, r0)] = log_sum(m, l);
             }
             ptx::tc_fence_before();  // O is read before the next tile's first P V, which p_full orders after this
         }

@@ -340,11 +340,11 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
                 *reinterpret_cast<float4*>(parts.o + at * D + c) = x;
                 if (c == 0) parts.ml[at] = make_float2(mm, ll);
             } else {
-                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                const float inv = inverse_sum(ll);
                 *reinterpret_cast<float4*>(o + cross_o_offset(g, b, j, row0 + r) + c) =
                     make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
                 if (c == 0 && lse)
-                    lse[cross_lse_offset(g, b, j, row0 + r)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                    lse[cross_lse_offset(g, b, j, row0 + r)] = log_sum(mm, ll);
             }
         }
     } else {
@@ -357,9 +357,9 @@ bra_cross_tf32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
                 store_row(parts.o + at * D, acc, h, 1.f, t4);
                 if (t4 == 0) parts.ml[at] = make_float2(m[h], l[h]);
             } else {
-                store_row(o + cross_o_offset(g, b, j, r), acc, h, l[h] > 0.f ? 1.f / l[h] : 0.f, t4);
+                store_row(o + cross_o_offset(g, b, j, r), acc, h, inverse_sum(l[h]), t4);
                 if (t4 == 0 && lse)
-                    lse[cross_lse_offset(g, b, j, r)] = l[h] > 0.f ? (m[h] + log2f(l[h])) * kLn2 : -INFINITY;
+                    lse[cross_lse_offset(g, b, j, r)] = log_sum(m[h], l[h]);
             }
         }
     }

@@ -13,6 +13,12 @@ namespace cross {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// What a row's sum of 2^(s' - m) ends as: the factor of O, and the natural log sum.  Only a
+// sum of zero is a row without valid states (O = 0, log sum -inf); a sum that is NaN,
+// of a row with a score that is, stays NaN in both.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
 // The exponent's offset of a row: its log sum in powers of two; a row without
 // valid states gets +inf, which makes its P zero.
 __device__ __forceinline__ float exponent_offset(float lse) {

@@ -329,8 +329,10 @@ size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
  *   lse_t = log sum_j exp(s_j).
  * State j is valid if j < kv_len[b] and kv_mask[b, j] != 0.  Invalid states
  * are not read: they may hold anything.  A token without valid states gets
- * O = 0 and lse = -infinity.  Any number of tokens runs: few (a decoder's next
- * token) split the states over the GPU.
+ * O = 0 and lse = -infinity; one with a score that is NaN or +infinity gets NaN
+ * in both, and so do its dQ and the dK and dV of all valid states that it reads.
+ * Any number of tokens runs: few (a decoder's next token) split the states over
+ * the GPU.
  *   kv_len     device int32 [B], or NULL (all Lk); values are clamped to [0, Lk]
  *   kv_mask    device uint8 [B, Lk] (any nonzero byte: valid), or NULL
  *   o          device [B, Lq, heads, d] of ``shape->dtype``, written

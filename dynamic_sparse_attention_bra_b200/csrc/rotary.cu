@@ -8,7 +8,8 @@
 // Angles of far positions do not fit fp32 (a position of 100000 leaves 2^-7 of a
 // turn).  A frequency in turns is kept as a 64-bit fraction F; position x F modulo
 // 2^64 is then the angle modulo a turn, whole turns wrapping away, at the cost of
-// two integer multiply-adds and good to 2^-32 of a turn over all 32-bit positions.
+// two integer multiply-adds and good to 2^-31 of a turn over all 32-bit positions:
+// 2^-33 for F's last unit and 2^-32 for the half of the product that is cut off.
 // Sine and cosine of the reduced angle are fp32.
 //
 // Bound by HBM (Q and K are read and written once, in 16-byte vectors) and, with
@@ -50,13 +51,24 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[V]) {
     }
 }
 
-// A frequency (radians a position) as a fraction of a turn, times 2^64.
+// A frequency (radians a position) as a fraction of a turn, times 2^64, within one
+// unit: its 24-bit m times 1 / (2 pi) as a 128-bit fraction, of which the 64 bits below
+// the point are taken where its exponent puts the point (the multiplication by stored
+// bits of the constant of Payne and Hanek, "Radian reduction for trigonometric
+// functions", 1983).  A negative frequency is the negated fraction of its magnitude;
+// what is formed as 1 - |t| in fp64 would lose the bits that far positions need.
 __device__ __forceinline__ uint64_t turns_of(float f) {
-    // 1 / (2 pi) in two parts; f has 24 bits, so that f hi + the fma's rest is exact
-    const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
-    const double t = (double)f * hi, rest = fma((double)f, hi, -t) + (double)f * lo;
-    const double frac = t - floor(t);  // exact
-    return (uint64_t)(frac * 18446744073709551616.0) + (uint64_t)(int64_t)(rest * 18446744073709551616.0);
+    const uint64_t hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+    const uint32_t bits = __float_as_uint(f), field = bits >> 23 & 255u;
+    const uint64_t m = field ? bits & 0x7fffffu | 0x800000u : bits & 0x7fffffu;
+    const uint64_t low = m * lo, mid = m * hi, carry = __umul64hi(m, lo);
+    const uint64_t w1 = mid + carry, w2 = __umul64hi(m, hi) + (w1 < mid ? 1u : 0u);
+    // f = m 2^(field - 150), so that the point's bits of (w2, w1, low) start here
+    const int s = 214 - (int)(field ? field : 1u), r = s & 63;
+    if (s < 0 || s >= 192) return 0ull;  // (past the contract, or less than a unit)
+    const uint64_t a = s < 64 ? low : s < 128 ? w1 : w2, b = s < 64 ? w1 : s < 128 ? w2 : 0ull;
+    const uint64_t t = r ? a >> r | b << (64 - r) : a;
+    return bits >> 31 ? 0ull - t : t;
 }
 
 // PAIRED: a unit is two vectors (split halves); else one (interleaved).

@@ -480,6 +480,22 @@ def rotary_shape_for(q, k, heads: int, kv_heads: int, pairs, grid=None, pos=None
                           ko_row, ko_batch)
 
 
+def _check_positions(pos, B: int, L: int, step: int):
+    """``pos`` has its entries where ``step`` (0: shared) finds them; a tensor that is merely
+    large enough would turn entries by another's positions."""
+    n = pos.numel()
+    if B <= 1 or n == (B * step if step else L * 3):
+        return
+    if step:
+        fine = pos.dim() < 3 or n == pos.shape[0] * step
+    else:
+        fine = pos.shape[0] == 1 or (pos.dim() < 3 and n < B * L * 3)
+    if not fine:
+        raise ValueError(f"pos: {tuple(pos.shape)} is not what the shape says ({B} entries of {L} tokens, "
+                         f"{f'{step} elements apart' if step else 'sharing their positions'}); "
+                         "rotary_shape_for takes the positions that the calls will be given")
+
+
 def bra_rotary(shape: BraRotaryShape, q, k, pos, inv_freq, q_out, k_out, stream=None) -> None:
     """q_out, k_out = q, k turned by their positions: pos int32 [B or 1, L, 3]
     (time, height, width), or None for the shape's grid; inv_freq fp32, one for
@@ -496,6 +512,7 @@ def bra_rotary(shape: BraRotaryShape, q, k, pos, inv_freq, q_out, k_out, stream=
         _same_tokens(k, "k", wk, B, L, s.k_row, s.k_batch, dtype, dev)
         _same_tokens(k_out, "k_out", wk, B, L, s.ko_row, s.ko_batch, dtype, dev)
     if pos is not None:
+        _check_positions(pos, B, L, s.pos_batch)
         _dense(pos, "pos", torch.int32, (B - 1) * s.pos_batch + L * 3 if B else 0, dev)
     _dense(inv_freq, "inv_freq", torch.float32, sum(s.pairs), dev)
     _call("bra_rotary", _lib.bra_rotary, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(pos), _ptr(inv_freq),

@@ -302,10 +302,15 @@ def _same_tokens(t, name, width, B, L, row, batch, dtype, dev: int):
                      f"shape says ({dtype} of [{B}, {L}, {width}], steps {batch}, {row}, on cuda:{dev})")
 
 
-def _dense(t, name, dtype, numel, dev: int):
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
+def _dense(t, name, dtype, numel, dev: int, entry: int = 0):
+    """``t`` is contiguous with ``numel`` elements or more.  ``entry``: elements of a leading
+    entry, where a larger tensor has to have entries of that size (0: it need not)."""
+    n = t.numel()
+    if t.dtype is not dtype or t.get_device() != dev or n < numel or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on cuda:{dev}, got "
                          f"{t.dtype} of {tuple(t.shape)} on {t.device}")
+    if n != numel and entry and t.dim() > 1 and n != t.shape[0] * entry:
+        raise ValueError(f"{name}: the entries of {tuple(t.shape)} do not have the shape's {entry} elements")
 
 
 def _cuda_device(t, where: str) -> int:
@@ -374,9 +379,14 @@ def _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace):
     if kv_mask is not None:
         if kv_mask.dtype == torch.bool:
             kv_mask = kv_mask.view(torch.uint8)
-        _dense(kv_mask, "kv_mask", torch.uint8, s.B * s.Lk, dev)
+        _dense(kv_mask, "kv_mask", torch.uint8, s.B * s.Lk, dev, s.Lk if s.B > 1 else 0)
     _dense(workspace, "workspace", torch.uint8, bra_cross_workspace_bytes(s), dev)
     return dev, kv_mask
+
+
+def _dense_log_sums(lse, s, dev: int):
+    import torch
+    _dense(lse, "lse", torch.float32, s.B * s.heads * s.Lq, dev, s.heads * s.Lq if s.B * s.heads > 1 else 0)
 
 
 def bra_cross_workspace_bytes(shape: BraCrossShape) -> int:
@@ -387,13 +397,15 @@ def bra_cross_attend(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o, lse, wor
     """o [B, Lq, heads * d] (and lse fp32 [B, heads, Lq], or None) of q over the
     states k, v; kv_len int32 [B] and kv_mask uint8 or bool [B, Lk], or None,
     say which states are valid.  ``workspace``: bra_cross_workspace_bytes(shape)
-    bytes of uint8, zeroed once."""
+    bytes of uint8, zeroed once.  Outputs and masks may be larger (more entries, flat
+    memory), not with longer entries: those lie elsewhere."""
     import torch
     s = shape
     dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
-    _dense(o, "o", q.dtype, s.B * s.Lq * s.heads * s.d, dev)
+    each = s.Lq * s.heads * s.d
+    _dense(o, "o", q.dtype, s.B * each, dev, each if s.B > 1 else 0)
     if lse is not None:
-        _dense(lse, "lse", torch.float32, s.B * s.Lq * s.heads, dev)
+        _dense_log_sums(lse, s, dev)
     _call("bra_cross_attend", _lib.bra_cross_attend, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v),
           _ptr(kv_len), _ptr(kv_mask), _ptr(o), _ptr(lse), _ptr(workspace))
 
@@ -405,10 +417,10 @@ def bra_cross_attend_backward(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o,
     import torch
     s = shape
     dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
-    nq, nk = s.B * s.Lq * s.heads * s.d, s.B * s.Lk * s.kv_heads * s.d
+    nq, nk = s.Lq * s.heads * s.d, s.Lk * s.kv_heads * s.d
     for t, name, n in ((o, "o", nq), (grad_o, "grad_o", nq), (dq, "dq", nq), (dk, "dk", nk), (dv, "dv", nk)):
-        _dense(t, name, q.dtype, n, dev)
-    _dense(lse, "lse", torch.float32, s.B * s.Lq * s.heads, dev)
+        _dense(t, name, q.dtype, s.B * n, dev, n if s.B > 1 else 0)
+    _dense_log_sums(lse, s, dev)
     _call("bra_cross_attend_backward", _lib.bra_cross_attend_backward, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k),
           _ptr(v), _ptr(kv_len), _ptr(kv_mask), _ptr(o), _ptr(lse), _ptr(grad_o), _ptr(dq), _ptr(dk), _ptr(dv),
           _ptr(workspace))
@@ -527,9 +539,10 @@ def bra_dropout_add(x, residual, p: float, rng, y, unit: int = 1, stream=None) -
     import torch
     n, dev = x.numel(), _cuda_device(x, "dropout")
     dtype = _dtype_code(x)
+    each = n // x.shape[0] if x.dim() > 1 and x.shape[0] > 1 else 0
     for t, name in ((x, "x"), (residual, "residual"), (y, "y")):
         if t is not None:
-            _dense(t, name, x.dtype, n, dev)
+            _dense(t, name, x.dtype, n, dev, each)
     _dense(rng, "rng", torch.uint64 if rng.dtype == torch.uint64 else torch.int64, 2, dev)
     _call("bra_dropout_add", _lib.bra_dropout_add, dev, stream, dtype, n, unit, p, _ptr(rng), _ptr(x), _ptr(residual),
           _ptr(y))

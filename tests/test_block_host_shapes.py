@@ -57,3 +57,61 @@ def test_positions_that_a_shape_would_misread(calls, B, pos, shape_pos):
 ], ids=str)
 def test_positions_that_a_shape_reads(calls, B, pos, shape_pos):
     rotary(calls, B, positions(*pos), None if shape_pos is None else positions(*shape_pos))
+
+
+# --------------------------------------------------- tensors with more in an entry than the shape's
+
+def cross(calls, B=2, Lq=5, Lk=9, backward=True, **other):
+    """Both calls on well-formed tensors, but for those named."""
+    x = dict(kv_len=z(B, dtype=torch.int32), kv_mask=z(B, Lk, dtype=torch.uint8), o=z(B, Lq, 64),
+             lse=z(B, 2, Lq, dtype=torch.float32), grad_o=z(B, Lq, 64), dq=z(B, Lq, 64), dk=z(B, Lk, 64),
+             dv=z(B, Lk, 64))
+    x.update(other)
+    q, k = z(B, Lq, 64), z(B, Lk, 64)
+    s = bra.cross_shape_for(q, k, k, 2)
+    ws = z(bra.bra_cross_workspace_bytes(s), dtype=torch.uint8)
+    bra.bra_cross_attend(s, q, k, k, x["kv_len"], x["kv_mask"], x["o"], x["lse"], ws)
+    if backward:
+        bra.bra_cross_attend_backward(s, q, k, k, x["kv_len"], x["kv_mask"], x["o"], x["lse"], x["grad_o"], x["dq"],
+                                      x["dk"], x["dv"], ws)
+    assert calls == ["bra_cross_attend", "bra_cross_attend_backward"][:1 + backward]
+
+
+@pytest.mark.parametrize("name,shape", [("kv_mask", (2, 12)), ("o", (2, 8, 64)), ("lse", (2, 2, 8)), ("grad_o", (2, 8, 64)),
+                                        ("dq", (2, 8, 64)), ("dk", (2, 12, 64)), ("dv", (2, 12, 64)), ("kv_mask", (3, 8)),
+                                        ("o", (2, 2, 4, 64))], ids=str)
+def test_longer_entries_are_refused(calls, name, shape):
+    """A mask of the padded length, an output kept for longer calls: its entries lie elsewhere."""
+    t = z(*shape, dtype={"kv_mask": torch.uint8, "lse": torch.float32}.get(name, torch.bfloat16))
+    with pytest.raises(ValueError, match=name):
+        cross(calls, **{name: t})
+
+
+def test_longer_heads_of_one_entry_are_refused(calls):
+    with pytest.raises(ValueError, match="lse"):
+        cross(calls, B=1, lse=z(1, 2, 8, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("other", [
+    dict(o=z(4, 5, 64), lse=z(3, 2, 5, dtype=torch.float32), dq=z(2, 1, 5, 64), dk=z(5, 9, 64)),  # more entries
+    dict(o=z(1000), lse=z(100, dtype=torch.float32), kv_mask=z(50, dtype=torch.uint8)),             # flat memory
+    dict(kv_len=z(7, dtype=torch.int32), kv_mask=z(2, 3, 3, dtype=torch.bool)),
+    dict(B=1, o=z(1, 8, 64), kv_mask=z(1, 12, dtype=torch.uint8), dk=z(1, 12, 64)),                 # one entry's start
+    dict(Lq=0, o=z(2, 5, 64), dq=z(2, 0, 64)),
+], ids=str)
+def test_larger_tensors_that_begin_as_the_shape_says(calls, other):
+    cross(calls, **other)
+
+
+@pytest.mark.parametrize("which", ["residual", "y"])
+def test_dropout_refuses_longer_entries(calls, which):
+    x, rng = z(2, 5, 64), z(2, dtype=torch.int64)
+    t = dict(residual=z(2, 5, 64), y=z(2, 5, 64))
+    t[which] = z(2, 8, 64)
+    with pytest.raises(ValueError, match=which):
+        bra.bra_dropout_add(x, t["residual"], 0.1, rng, t["y"])
+    t[which] = z(3, 5, 64)
+    bra.bra_dropout_add(x, t["residual"], 0.1, rng, t["y"])
+    t[which] = z(1000)
+    bra.bra_dropout_add(x, t["residual"], 0.1, rng, t["y"])
+    assert calls == ["bra_dropout_add"] * 2

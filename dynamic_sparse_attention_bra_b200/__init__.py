@@ -380,7 +380,7 @@ def _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace):
         if kv_mask.dtype == torch.bool:
             kv_mask = kv_mask.view(torch.uint8)
         _dense(kv_mask, "kv_mask", torch.uint8, s.B * s.Lk, dev, s.Lk if s.B > 1 else 0)
-    _dense(workspace, "workspace", torch.uint8, bra_cross_workspace_bytes(s), dev)
+    _dense(workspace, "workspace", torch.uint8, _cross_workspace_bytes_on(s, dev), dev)
     return dev, kv_mask
 
 
@@ -389,7 +389,17 @@ def _dense_log_sums(lse, s, dev: int):
     _dense(lse, "lse", torch.float32, s.B * s.heads * s.Lq, dev, s.heads * s.Lq if s.B * s.heads > 1 else 0)
 
 
+def _cross_workspace_bytes_on(shape, dev: int) -> int:
+    """The size for device ``dev``, by whose number of SMs its kernels split their work."""
+    import torch
+    if dev == torch.cuda.current_device():
+        return bra_cross_workspace_bytes(shape)
+    with torch.cuda.device(dev):
+        return bra_cross_workspace_bytes(shape)
+
+
 def bra_cross_workspace_bytes(shape: BraCrossShape) -> int:
+    """Bytes of workspace that ``shape`` needs on the current device."""
     return int(_lib.bra_cross_workspace_bytes(ctypes.byref(shape)))
 
 
@@ -445,10 +455,9 @@ def cross_attention(q, k, v, heads: int, kv_heads: int | None = None, kv_len=Non
     kernels end), then runs ``bra_cross_attend``."""
     import torch
     shape = cross_shape_for(q, k, v, heads, kv_heads, scale)
-    nbytes = bra_cross_workspace_bytes(shape)
+    nbytes = _cross_workspace_bytes_on(shape, _cuda_device(q, "cross attention"))
     if nbytes == 0:
         raise BraError(BRA_ERR_INVALID_ARG if shape.d in (32, 64, 128) else BRA_ERR_UNSUPPORTED, "cross_attention")
-    _cuda_device(q, "cross attention")
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=q.device)
     with torch.cuda.stream(stream):  # None: as it is

@@ -115,3 +115,33 @@ def test_dropout_refuses_longer_entries(calls, which):
     t[which] = z(1000)
     bra.bra_dropout_add(x, t["residual"], 0.1, rng, t["y"])
     assert calls == ["bra_dropout_add"] * 2
+
+
+# ------------------------------------------------------------------ the workspace's device
+
+def test_the_workspace_s_size_is_that_of_the_tensors_device(monkeypatch):
+    """Device 1, with more SMs than the current device 0, splits further and needs more."""
+    current, made = [0], []
+
+    @contextlib.contextmanager
+    def device(i):
+        current.append(i)
+        yield
+        current.pop()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(bra, "_cuda_device", lambda t, where: 1)
+    monkeypatch.setattr(bra, "_same_tokens", lambda *a: None)
+    monkeypatch.setattr(bra, "_dense", lambda t, name, dtype, numel, dev, entry=0: made.append((name, numel)))
+    monkeypatch.setattr(bra, "bra_cross_workspace_bytes", lambda s: 1000 + 1000 * current[-1])
+    monkeypatch.setattr(bra, "_call", lambda *a: None)
+    q, k = z(2, 5, 64), z(2, 9, 64)
+    s = bra.cross_shape_for(q, k, k, 2)
+    bra.bra_cross_attend(s, q, k, k, None, None, q, None, q)
+    bra.bra_cross_attend_backward(s, q, k, k, None, None, q, q, q, q, k, k, q)
+    assert [n for name, n in made if name == "workspace"] == [2000, 2000]
+    sizes = []
+    monkeypatch.setattr(torch, "zeros", lambda n, **kw: sizes.append(n) or q)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    bra.cross_attention(q, k, k, 2)
+    assert sizes == [2000] and current == [0]

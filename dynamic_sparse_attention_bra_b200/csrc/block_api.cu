@@ -36,7 +36,8 @@ bra_status make_cross(const bra_cross_shape* s, CrossGeom* g) {
     if (s->B < 0 || s->Lq < 0 || s->Lk < 0 || s->heads <= 0 || s->kv_heads <= 0 || s->d <= 0)
         return BRA_ERR_INVALID_ARG;
     if (s->heads % s->kv_heads || !known_dtype(s->dtype)) return BRA_ERR_INVALID_ARG;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return BRA_ERR_INVALID_ARG;
+    // the kernels' exponents are powers of two: scale log2(e) is finite too
+    if (!(s->scale > 0.f) || !std::isfinite(s->scale * 1.44269504f)) return BRA_ERR_INVALID_ARG;
     if (s->d != 32 && s->d != 64 && s->d != 128) return BRA_ERR_UNSUPPORTED;
     if (s->B > 65535 || s->heads > 1024 || s->Lk > 1 << 28 || (int64_t)s->Lq * s->heads > 1 << 28)
         return BRA_ERR_UNSUPPORTED;

@@ -311,7 +311,7 @@ typedef struct {
     int B, Lq, Lk;
     int heads, kv_heads, d;
     int dtype;   /* a bra_dtype */
-    float scale; /* of the logits; finite and positive, 1/sqrt(d) as a rule */
+    float scale; /* of the logits; positive and below 2^127, 1/sqrt(d) as a rule */
     int64_t q_row, q_batch, k_row, k_batch, v_row, v_batch;
 } bra_cross_shape;
 

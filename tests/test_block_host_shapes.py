@@ -145,3 +145,16 @@ def test_the_workspace_s_size_is_that_of_the_tensors_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     bra.cross_attention(q, k, k, 2)
     assert sizes == [2000] and current == [0]
+
+
+# ------------------------------------------------------------------ scales
+
+@pytest.mark.parametrize("scale,code", [(2.4e38, bra.BRA_ERR_INVALID_ARG), (3.4e38, bra.BRA_ERR_INVALID_ARG),
+                                        (1.7e38, bra.BRA_OK), (1e-45, bra.BRA_OK)])
+def test_scales_whose_powers_of_two_overflow(scale, code):
+    """The kernels multiply by scale log2(e), which has to be finite too."""
+    q = z(0, 5, 64)
+    s = bra.cross_shape_for(q, q, q, 2, scale=scale)
+    p = 1 << 20  # never followed: there is no entry
+    assert bra._lib.bra_cross_attend(s, *([p] * 8), None) == code
+    assert (bra.bra_cross_workspace_bytes(s) == 0) == (code != bra.BRA_OK)

@@ -461,6 +461,7 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             __nv_bfloat16* orow = in ? o + cross_o_offset(g, x.b, x.j, r0) : o;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
+                __syncwarp();  // rows past the last store nothing, but stay with their warp for its loads
                 uint32_t r[16];
                 if (x.nb > 0) {
                     ptx::tmem_ld16(cols + C::kO + c, r);
@@ -469,12 +470,11 @@ bra_cross_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 #pragma unroll
                     for (int e = 0; e < 16; ++e) r[e] = 0u;
                 }
-                if (!in) continue;
-                if (p.splits > 1) {
+                if (in && p.splits > 1) {
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
                         *reinterpret_cast<uint4*>(parts.o + part * D + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
-                } else {
+                } else if (in) {
                     uint32_t w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)

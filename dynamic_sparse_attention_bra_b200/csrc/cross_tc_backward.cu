@@ -496,9 +496,9 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
             const size_t elems = (size_t)g.B * g.Lk * g.kv_heads * D;
 #pragma unroll 1
             for (int c = mine * (D / kEach); c < (mine + 1) * (D / kEach); c += 8) {
+                __syncwarp();  // rows past the last store nothing, but stay with their warp for its loads
                 uint32_t a1[8], a2[8];
                 if (x.nb > 0) ptx::tmem_load_pair(lanes + C::kAcc1 + c, lanes + C::kAcc2 + c, a1, a2);
-                if (!in) continue;
                 float f1[8], f2[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -507,14 +507,14 @@ bra_cross_tc_backward_kernel(const __grid_constant__ CUtensorMap tr1, const __gr
                     if (!STATES) f1[e] = fmaf(-rest, f2[e], f1[e]);
                     f1[e] *= g.scale;
                 }
-                if (STATES && p.splits > 1) {
+                if (STATES && in && p.splits > 1) {
                     float* out = parts + (size_t)x.split * 2 * elems + at + c;
 #pragma unroll
                     for (int e = 0; e < 8; e += 4) {
                         *reinterpret_cast<float4*>(out + e) = make_float4(f1[e], f1[e + 1], f1[e + 2], f1[e + 3]);
                         *reinterpret_cast<float4*>(out + elems + e) = make_float4(f2[e], f2[e + 1], f2[e + 2], f2[e + 3]);
                     }
-                } else {
+                } else if (in) {
                     *reinterpret_cast<uint4*>(out1 + at + c) =
                         make_uint4(ptx::pack_bf16x2(f1[0], f1[1]), ptx::pack_bf16x2(f1[2], f1[3]),
                                    ptx::pack_bf16x2(f1[4], f1[5]), ptx::pack_bf16x2(f1[6], f1[7]));

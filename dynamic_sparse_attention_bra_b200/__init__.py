@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 __all__ = [
     "BraError", "BraShape", "shape_for", "bra_workspace_bytes", "bra_route", "bra_attend",
@@ -452,8 +453,13 @@ def cross_attention(q, k, v, heads: int, kv_heads: int | None = None, kv_len=Non
 
     Allocates o, lse and a zeroed workspace with torch on q's device (as
     ``stream``'s, where one is given: what is freed is not used again before the
-    kernels end), then runs ``bra_cross_attend``."""
+    kernels end), then runs ``bra_cross_attend``.  The results carry no autograd
+    graph (a warning says so where an input asks for gradients): those come from
+    ``bra_cross_attend_backward`` with this o and lse."""
     import torch
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        warnings.warn("cross_attention returns o and lse without an autograd graph; the gradients of q, k and v are "
+                      "bra_cross_attend_backward's", stacklevel=2)
     shape = cross_shape_for(q, k, v, heads, kv_heads, scale)
     nbytes = _cross_workspace_bytes_on(shape, _cuda_device(q, "cross attention"))
     if nbytes == 0:

@@ -2,6 +2,7 @@
 operators' Python layer refuses before it hands pointers on.  The device checks are
 replaced, so that all of it runs on CPU tensors; nothing reaches a kernel."""
 import contextlib
+import warnings
 
 import pytest
 import torch
@@ -158,3 +159,20 @@ def test_scales_whose_powers_of_two_overflow(scale, code):
     p = 1 << 20  # never followed: there is no entry
     assert bra._lib.bra_cross_attend(s, *([p] * 8), None) == code
     assert (bra.bra_cross_workspace_bytes(s) == 0) == (code != bra.BRA_OK)
+
+
+# ------------------------------------------------------------------ gradients that the wrapper does not give
+
+def test_the_wrapper_says_that_it_gives_no_gradients(calls, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    q, k = z(2, 5, 64), z(2, 9, 64)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        bra.cross_attention(q, k, k, 2)
+        with torch.no_grad():
+            bra.cross_attention(q.requires_grad_(), k, k, 2)
+    for args in ((q, k, k), (q.detach(), k.requires_grad_(), k), (q.detach(), k.detach(), k)):
+        with pytest.warns(UserWarning, match="bra_cross_attend_backward"):
+            o, lse = bra.cross_attention(*args, 2)
+        assert not o.requires_grad
+    assert len(calls) == 5

@@ -343,7 +343,9 @@ size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
  * bf16: products on tensor cores with fp32 sums, the softmax in fp32, P
  * rounded once to bf16 as an operand, O rounded once.  fp32: each product of
  * two factors as three tf32 products of their parts (relative error 2^-20),
- * sums and softmax in fp32.  The same inputs give the same bits.
+ * sums and softmax in fp32; a valid factor that is infinite, or finite and of
+ * 2^128 (1 - 2^-13) or more, has no such parts and makes NaN of the sums that it
+ * enters.  The same inputs give the same bits.
  * Errors: BRA_ERR_INVALID_ARG, BRA_ERR_UNSUPPORTED (another d, or past the
  * limits), BRA_ERR_CUDA.
  */

@@ -62,3 +62,48 @@ def test_a_valid_key_with_nan(size, dtype):
         assert torch.equal(out[x].view(B, Lq, h, d).isnan(), nan[..., None].expand(-1, -1, -1, d)), x
     assert torch.equal(out["lse"].isnan(), nan.transpose(1, 2))
     assert bool((out["lse"][0] == -math.inf).all())
+
+
+@pytest.mark.parametrize("value", [float("inf"), -3.4028e38])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_a_value_past_what_fp32_can_split_stays_in_its_channel(size, dtype, value):
+    """In fp32 such a value's parts make NaN, in bf16 the sums follow IEEE; either way the other
+    channels, heads and entries keep their bits, and so does lse."""
+    B, Lq, Lk, h, kv, d = size
+    q, k, v, g, m, ok = inputs(size, dtype)
+    a = run(q, k, v, h, kv, None, m)
+    v2 = v.clone()
+    v2[1, Lk // 2, 3] = value
+    b = run(q, k, v2, h, kv, None, m)
+    touched = torch.zeros((B, Lq, h, d), dtype=torch.bool, device="cuda")
+    touched[1, :, :h // kv, 3] = True
+    x, y = (t["o"].view(B, Lq, h, d) for t in (a, b))
+    assert torch.equal(x[~touched], y[~touched]) and torch.equal(a["lse"], b["lse"])
+    if dtype == "f32":
+        assert bool(y[touched].isnan().all())
+    elif math.isinf(value):
+        assert not bool(torch.isfinite(y[touched]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_an_infinite_key_s_tokens_say_nan(size, dtype):
+    """Scores of +-infinity: NaN where they are +infinity, nothing of the state
+    where they are -infinity (NaN in fp32, whose parts know no infinity)."""
+    B, Lq, Lk, h, kv, d = size
+    q, k, v, g, m, ok = inputs(size, dtype)
+    k[:, Lk // 2, 0] = float("inf")
+    up = (q.view(B, Lq, h, d)[..., :h // kv, 0] > 0)
+    out = run(q, k, v, h, kv, None, m)
+    lse = out["lse"][:, :h // kv].transpose(1, 2)[1:]
+    if dtype == "f32":
+        assert bool(lse.isnan().all())
+    else:
+        assert torch.equal(lse.isnan(), up[1:])
+        m2 = m.clone()
+        m2[:, Lk // 2] = 0
+        other = run(q, k, v, h, kv, None, m2)
+        down = ~up[1:]
+        assert bool((lse[down] - other["lse"][:, :h // kv].transpose(1, 2)[1:][down]).abs().max() <= 1e-3)
+    assert bool((out["lse"][0] == -math.inf).all())

@@ -1,34 +1,10 @@
 #include "cross_map.h"
 
-#include <mutex>
-
 namespace bra {
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encoder() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-}  // namespace
 
 bool encode_heads_map(CUtensorMap* map, const void* base, int B, int L, int heads, int d, long long row,
                       long long batch, int box_tokens, int box_heads) {
-    EncodeTiledFn fn = encoder();
+    const EncodeTiledFn fn = tensor_map_encoder();
     const int box_c = d < 64 ? 32 : 64;
     if (!fn || d % box_c != 0 || box_tokens > 256 || box_heads > 256) return false;
     if (row <= 0 || row >= 1LL << 38 || batch < 0 || batch >= 1LL << 38) return false;

@@ -48,12 +48,6 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
-}  // namespace ptx
-}  // namespace bra
-
-namespace bra {
-namespace ptx {
-
 // 32 lanes x 64 / 128 consecutive fp32 columns, loaded when the call returns.
 // Loads and wait are one statement: registers that a separate wait names again
 // cost a move each (0.9 moves a score, a quarter of a softmax's time, in
@@ -104,16 +98,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-}  // namespace ptx
-}  // namespace bra
-
-namespace bra {
-namespace ptx {
-
-// The same products and commit for a whole converged warp, one elected lane of
-// which issues them (always the same one).  Their operands then stay in the
-// warp's uniform registers; behind a branch on the lane they are moved there anew
-// for each product.
+// D[tmem] (+)= A B (kind::f16, bf16 factors, fp32 sums) and the commit of what was issued,
+// for a whole converged warp, one elected lane of which issues them (always the same
+// one).  Their operands then stay in the warp's uniform registers; behind a branch on
+// the lane they are moved there anew for each product.
 __device__ __forceinline__ void warp_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
     asm volatile(

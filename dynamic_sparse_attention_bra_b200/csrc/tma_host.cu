@@ -3,14 +3,8 @@
 #include <mutex>
 
 namespace bra {
-namespace {
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encoder() {
+EncodeTiledFn tensor_map_encoder() {
     static std::once_flag once;
     static EncodeTiledFn fn = nullptr;
     std::call_once(once, [] {
@@ -24,12 +18,10 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-}  // namespace
-
 bool encode_region_map(CUtensorMap* map, const void* base, int B, int H, int W, int C, int box_w,
                        int box_h, int box_c) {
     if (box_c != 32 && box_c != 64) return false;
-    EncodeTiledFn fn = encoder();
+    const EncodeTiledFn fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)C, (cuuint64_t)W, (cuuint64_t)H, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)C * 2, (cuuint64_t)W * C * 2,
@@ -44,7 +36,7 @@ bool encode_region_map(CUtensorMap* map, const void* base, int B, int H, int W, 
 
 bool encode_region_major_map(CUtensorMap* map, const void* base, int B, int H, int W, int C, int ws, int hs,
                              int S) {
-    EncodeTiledFn fn = encoder();
+    const EncodeTiledFn fn = tensor_map_encoder();
     if (!fn || H != hs * S || W != ws * S) return false;
     // dims: channel, x in region, y in region, region column, (image, region row)
     const cuuint64_t dims[5] = {(cuuint64_t)C, (cuuint64_t)ws, (cuuint64_t)hs, (cuuint64_t)S, (cuuint64_t)B * S};
@@ -58,7 +50,7 @@ bool encode_region_major_map(CUtensorMap* map, const void* base, int B, int H, i
 }
 
 bool encode_halo_map(CUtensorMap* map, const void* base, int B, int H, int W, int C, int box_w, int box_h) {
-    EncodeTiledFn fn = encoder();
+    const EncodeTiledFn fn = tensor_map_encoder();
     if (!fn || C % 64 != 0) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)C, (cuuint64_t)W, (cuuint64_t)H, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)C * 2, (cuuint64_t)W * C * 2, (cuuint64_t)H * W * C * 2};

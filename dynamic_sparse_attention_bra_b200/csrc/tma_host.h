@@ -7,6 +7,13 @@
 
 namespace bra {
 
+// The driver's tensor-map encoder, or null where the entry point is missing.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
+
 // Tensor map whose box is box_c channels (32: one head, 64-byte swizzle in
 // shared memory; 64: two heads, 128-byte swizzle) of a box_w x box_h block of
 // tokens of one image.  Returns false if the driver entry point is missing or

@@ -303,14 +303,18 @@ def _same_tokens(t, name, width, B, L, row, batch, dtype, dev: int):
                      f"shape says ({dtype} of [{B}, {L}, {width}], steps {batch}, {row}, on cuda:{dev})")
 
 
-def _dense(t, name, dtype, numel, dev: int, entry: int = 0):
-    """``t`` is contiguous with ``numel`` elements or more.  ``entry``: elements of a leading
-    entry, where a larger tensor has to have entries of that size (0: it need not)."""
+def _dense(t, name, dtype, numel, dev: int) -> bool:
+    """``t`` is contiguous with ``numel`` elements or more; whether it has just these."""
     n = t.numel()
     if t.dtype is not dtype or t.get_device() != dev or n < numel or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on cuda:{dev}, got "
                          f"{t.dtype} of {tuple(t.shape)} on {t.device}")
-    if n != numel and entry and t.dim() > 1 and n != t.shape[0] * entry:
+    return n == numel
+
+
+def _entries(t, name, count: int, entry: int):
+    """A larger ``t`` has entries of the shape's ``entry`` elements, where there is more than one."""
+    if count > 1 and entry and t.dim() > 1 and t.numel() != t.shape[0] * entry:
         raise ValueError(f"{name}: the entries of {tuple(t.shape)} do not have the shape's {entry} elements")
 
 
@@ -328,16 +332,28 @@ def _current_stream(dev: int) -> int:
     return direct(dev) if direct is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
+_query_device = None
+
+
+def _current_device() -> int:
+    """torch.cuda.current_device(), by the direct query where this torch has it."""
+    global _query_device
+    if _query_device is None:
+        import torch
+        _query_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _query_device()
+
+
 def _call(where: str, fn, dev: int, stream, *args):
     """``fn(*args, stream)`` with device ``dev`` current; None is its current stream."""
-    import torch
     if stream is None:
         raw = _current_stream(dev)
     else:
         raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, raw)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, raw)
     if status != BRA_OK:
@@ -380,21 +396,22 @@ def _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace):
     if kv_mask is not None:
         if kv_mask.dtype == torch.bool:
             kv_mask = kv_mask.view(torch.uint8)
-        _dense(kv_mask, "kv_mask", torch.uint8, s.B * s.Lk, dev, s.Lk if s.B > 1 else 0)
+        _dense(kv_mask, "kv_mask", torch.uint8, B * Lk, dev) or _entries(kv_mask, "kv_mask", B, Lk)
     _dense(workspace, "workspace", torch.uint8, _cross_workspace_bytes_on(s, dev), dev)
     return dev, kv_mask
 
 
 def _dense_log_sums(lse, s, dev: int):
     import torch
-    _dense(lse, "lse", torch.float32, s.B * s.heads * s.Lq, dev, s.heads * s.Lq if s.B * s.heads > 1 else 0)
+    each = s.heads * s.Lq
+    _dense(lse, "lse", torch.float32, s.B * each, dev) or _entries(lse, "lse", s.B * s.heads, each)
 
 
 def _cross_workspace_bytes_on(shape, dev: int) -> int:
     """The size for device ``dev``, by whose number of SMs its kernels split their work."""
-    import torch
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         return bra_cross_workspace_bytes(shape)
+    import torch
     with torch.cuda.device(dev):
         return bra_cross_workspace_bytes(shape)
 
@@ -414,7 +431,7 @@ def bra_cross_attend(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o, lse, wor
     s = shape
     dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
     each = s.Lq * s.heads * s.d
-    _dense(o, "o", q.dtype, s.B * each, dev, each if s.B > 1 else 0)
+    _dense(o, "o", q.dtype, s.B * each, dev) or _entries(o, "o", s.B, each)
     if lse is not None:
         _dense_log_sums(lse, s, dev)
     _call("bra_cross_attend", _lib.bra_cross_attend, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v),
@@ -430,7 +447,7 @@ def bra_cross_attend_backward(shape: BraCrossShape, q, k, v, kv_len, kv_mask, o,
     dev, kv_mask = _cross_inputs(s, q, k, v, kv_len, kv_mask, workspace)
     nq, nk = s.Lq * s.heads * s.d, s.Lk * s.kv_heads * s.d
     for t, name, n in ((o, "o", nq), (grad_o, "grad_o", nq), (dq, "dq", nq), (dk, "dk", nk), (dv, "dv", nk)):
-        _dense(t, name, q.dtype, s.B * n, dev, n if s.B > 1 else 0)
+        _dense(t, name, q.dtype, s.B * n, dev) or _entries(t, name, s.B, n)
     _dense_log_sums(lse, s, dev)
     _call("bra_cross_attend_backward", _lib.bra_cross_attend_backward, dev, stream, ctypes.byref(s), _ptr(q), _ptr(k),
           _ptr(v), _ptr(kv_len), _ptr(kv_mask), _ptr(o), _ptr(lse), _ptr(grad_o), _ptr(dq), _ptr(dk), _ptr(dv),
@@ -554,10 +571,9 @@ def bra_dropout_add(x, residual, p: float, rng, y, unit: int = 1, stream=None) -
     import torch
     n, dev = x.numel(), _cuda_device(x, "dropout")
     dtype = _dtype_code(x)
-    each = n // x.shape[0] if x.dim() > 1 and x.shape[0] > 1 else 0
     for t, name in ((x, "x"), (residual, "residual"), (y, "y")):
-        if t is not None:
-            _dense(t, name, x.dtype, n, dev, each)
+        if t is not None and not _dense(t, name, x.dtype, n, dev) and x.dim() > 1 and n:
+            _entries(t, name, x.shape[0], n // x.shape[0])
     _dense(rng, "rng", torch.uint64 if rng.dtype == torch.uint64 else torch.int64, 2, dev)
     _call("bra_dropout_add", _lib.bra_dropout_add, dev, stream, dtype, n, unit, p, _ptr(rng), _ptr(x), _ptr(residual),
           _ptr(y))

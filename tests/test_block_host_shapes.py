@@ -15,7 +15,7 @@ def calls(monkeypatch):
     """The C calls that pass the checks, in place of making them."""
     made = []
     monkeypatch.setattr(bra, "_cuda_device", lambda t, where: -1)  # what get_device() says of CPU tensors
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(bra, "_current_device", lambda: -1)
     monkeypatch.setattr(bra, "_call", lambda where, fn, dev, stream, *args: made.append(where))
     return made
 
@@ -129,11 +129,11 @@ def test_the_workspace_s_size_is_that_of_the_tensors_device(monkeypatch):
         current.append(i)
         yield
         current.pop()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(bra, "_current_device", lambda: current[-1])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(bra, "_cuda_device", lambda t, where: 1)
     monkeypatch.setattr(bra, "_same_tokens", lambda *a: None)
-    monkeypatch.setattr(bra, "_dense", lambda t, name, dtype, numel, dev, entry=0: made.append((name, numel)))
+    monkeypatch.setattr(bra, "_dense", lambda t, name, dtype, numel, dev: not made.append((name, numel)))
     monkeypatch.setattr(bra, "bra_cross_workspace_bytes", lambda s: 1000 + 1000 * current[-1])
     monkeypatch.setattr(bra, "_call", lambda *a: None)
     q, k = z(2, 5, 64), z(2, 9, 64)

@@ -23,11 +23,12 @@
 //
 // d = 32: a block costs a tile's threads its waits and TMEM latencies besides the
 // exponentials, so four tiles share an SM (2 x 16,384 rows of 2 heads over 4096
-// states: 109 us for 132 with two tiles and blocks of 128).
+// states: 107 us for 132 with two tiles and blocks of 128).
 //
 // Bound by the exponentials (16 a clock and SM) for d = 32, where they would take 61
-// of those 109 us, by them and the products for d = 128 (4 x 2048 tokens of 16 heads
-// on 4, up to 2048 states each: 106 us, 58 % of a large product's rate).
+// of those 107 us, by them and the products for d = 128 (4 x 2048 tokens of 16 heads
+// on 4, up to 2048 states each: 103 to 119 us by the power
+// that a run gets, 52 to 60 % of a large product's rate).
 // Every mbarrier wait is bounded; on expiry the kernel records kDevTimeout, stops
 // all roles, drains its products and frees TMEM.
 #include "cross_map.h"

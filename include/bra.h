@@ -328,9 +328,9 @@ size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
  *   s_j = scale <q_t, k_j>,  O_t = sum_j softmax_j(s) v_j,
  *   lse_t = log sum_j exp(s_j).
  * State j is valid if j < kv_len[b] and kv_mask[b, j] != 0.  Invalid states
- * reach no result and may hold anything, but all Lk rows of K and V are readable
- * memory: calls of many rows load whole blocks of them, which of a cache whose
- * tail is not there yet only a shape with a smaller Lk leaves out.  A token without valid states gets
+ * reach no result and may hold anything, but all Lk rows of K and V have to be
+ * readable memory: calls of many rows load whole blocks of them.  (The tail of a
+ * cache that is not mapped yet is left out by a smaller Lk.)  A token without valid states gets
  * O = 0 and lse = -infinity; one with a score that is NaN or +infinity gets NaN
  * in both, and so do its dQ and the dK and dV of all valid states that it reads.
  * Any number of tokens runs: few (a decoder's next token) split the states over

@@ -1,5 +1,6 @@
 // Cross attention and its gradients in fp32 on tensor cores (the formulas are
-// those of the bf16 kernels).  Every fp32 factor x is split into x rounded to tf32
+// those of the bf16 kernels).  Every fp32 factor x is split (as by Dekker, "A floating-
+// point technique for extending the available precision", 1971) into x rounded to tf32
 // and the rest, x - that, which is exact; a product of two factors is then three tf32 products,
 //   x y = xh yh + xh yl + xl yh  (+ xl yl, below 2^-20 of x y),
 // summed in fp32: some 2^-21 of relative error a factor, the order of fp32's own

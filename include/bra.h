@@ -330,11 +330,11 @@ size_t bra_cross_workspace_bytes(const bra_cross_shape* shape);
  * State j is valid if j < kv_len[b] and kv_mask[b, j] != 0.  Invalid states
  * reach no result and may hold anything, but all Lk rows of K and V have to be
  * readable memory: calls of many rows load whole blocks of them.  (The tail of a
- * cache that is not mapped yet is left out by a smaller Lk.)  A token without valid states gets
- * O = 0 and lse = -infinity; one with a score that is NaN or +infinity gets NaN
- * in both, and so do its dQ and the dK and dV of all valid states that it reads.
- * Any number of tokens runs: few (a decoder's next token) split the states over
- * the GPU.
+ * cache that is not mapped yet is left out by a smaller Lk.)  A token without
+ * valid states gets O = 0 and lse = -infinity; one with a score that is NaN or
+ * +infinity gets NaN in both, and so do its dQ and the dK and dV of all valid
+ * states that it reads.  Any number of tokens runs: few (a decoder's next token)
+ * split the states over the GPU.
  *   kv_len     device int32 [B], or NULL (all Lk); values are clamped to [0, Lk]
  *   kv_mask    device uint8 [B, Lk] (any nonzero byte: valid), or NULL
  *   o          device [B, Lq, heads, d] of ``shape->dtype``, written
